@@ -78,8 +78,9 @@ typedef struct {
                            data-type decoupling: a registered QDQ function
                            evaluates a new type's accuracy), through
                            ar_qdq_rtn with V = beta = NULL (alpha clips the
-                           group maximum); every other entry point returns
-                           AR_ERR_UNSUPPORTED for them:
+                           group maximum; packed MXFP4 has entry points of
+                           its own, ar_pack_mxfp4 and below); every other
+                           entry point returns AR_ERR_UNSUPPORTED for them:
                            AR_FMT_FP8_E4M3: bits 8, s = alpha*max|W_g|/448,
                              codes are E4M3 bytes, zero written as 0;
                            AR_FMT_MXFP4: bits 4, group_size 32, s = 2^e with
@@ -198,6 +199,69 @@ AR_API ar_status ar_pack_int4(const void* W, ar_dtype wt, int64_t N, int64_t K, 
 AR_API ar_status ar_w4a16_gemm(const void* X, ar_dtype xt, int64_t M, int64_t K,
                         const uint8_t* packed, const float* scale, const uint8_t* zero, int64_t N,
                         int32_t group_size, void* Y, ar_dtype yt, void* stream);
+
+/* Packed MXFP4: the deployment form of the format that ar_qdq_rtn evaluates
+ * with AR_FMT_MXFP4, for weights and for activations.  Along a row of K
+ * elements (K a multiple of 32) each block of 32 shares 2^e; with m =
+ * max|x_b|, e = max(floor(log2 m) - 2, -127), 0 for m = 0.  An element is the
+ * E2M1 value nearest x / 2^e (ties to the even code, saturating at 6, no
+ * negative zero).
+ *  packed  DEVICE uint8 [rows, K/2]: byte j of a row holds code 2j in its low
+ *          nibble and code 2j+1 in its high nibble; 16-byte aligned
+ *  scale   DEVICE uint8 [rows, K/32]: e + 127; 255 (codes 0) for a block whose
+ *          maximum is NaN, infinite or beyond the fp32 range: its values are NaN
+ * Zero rows are an empty problem and return AR_OK (pointers may be NULL).
+ * The six calls below allocate nothing, so they may be captured into a HIP
+ * graph, and are stream-ordered without synchronization.  Common errors:
+ * AR_ERR_INVALID_ARG for a NULL pointer, negative rows or a K that is no
+ * positive multiple of 32; AR_ERR_UNSUPPORTED for K >= 2^30, more than 2^34
+ * elements (2^40 of Y) or a pointer that is not 16-byte aligned (scales and Y: any).
+ * Outputs must not overlap inputs. */
+
+/* Quantize W DEVICE [N, K] (fp32 or bf16) to packed MXFP4: the codes of
+ * ar_qdq_rtn, two per byte.  alpha DEVICE fp32 [N, K/32] clip factors, m =
+ * |alpha * max|x_b||, nullable (= 1).  (For block maxima below 2^-125 ar_qdq_rtn
+ * takes exponents under -127, which the scale byte cannot hold; here e stays
+ * at -127.) */
+AR_API ar_status ar_pack_mxfp4(const void* W, ar_dtype wt, int64_t N, int64_t K, const float* alpha,
+                        uint8_t* packed, uint8_t* scale, void* stream);
+
+/* The values of packed MXFP4, W DEVICE [N, K] of dtype wt (both hold every
+ * value below the fp32 range exactly). */
+AR_API ar_status ar_unpack_mxfp4(const uint8_t* packed, const uint8_t* scale, int64_t N, int64_t K, void* W,
+                          ar_dtype wt, void* stream);
+
+/* The norm in front of a quantized product, with the residual it follows:
+ *     r = x + delta_scale * delta   (fp32),   h = r / sqrt(mean(r^2) + eps) * w
+ * per row; h leaves as packed MXFP4.  Its codes are those of h in 64 bits.
+ *  x      DEVICE bf16 [M, H], H a multiple of 32 and at most 32768
+ *         (AR_ERR_UNSUPPORTED beyond)
+ *  delta  DEVICE [M, H] of delta_dtype, nullable (r = x; delta_scale and
+ *         delta_dtype are then not used)
+ *  w      DEVICE fp32 [H], nullable (= 1);  eps >= 0
+ *  r_out  DEVICE bf16 [M, H], the rounded r, nullable */
+AR_API ar_status ar_rmsnorm_mxfp4(const void* x, const void* delta, ar_dtype delta_dtype, float delta_scale,
+                           const float* w, int64_t M, int64_t H, float eps, void* r_out,
+                           uint8_t* packed, uint8_t* scale, void* stream);
+
+/* The gated activation in front of the down projection, h = silu(gate) * up,
+ * silu(a) = a / (1 + exp(-a)), as packed MXFP4 with the codes of h in 64 bits.
+ *  gate, up  DEVICE bf16 [M, F], rows ld_gate / ld_up elements apart (at least
+ *            F, multiples of 8), so both may be halves of one [M, 2F] product */
+AR_API ar_status ar_swiglu_mxfp4(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int64_t M,
+                          int64_t F, uint8_t* packed, uint8_t* scale, void* stream);
+
+/* MXFP4-weight GEMM on bf16 activations: Y[m, n] = sum_k X[m, k] W[n, k] with
+ * W the values of packed [N, K/2] / scale [N, K/32] (exact in bf16) and fp32
+ * accumulation.  X DEVICE bf16 [M, K], Y DEVICE [M, N] of dtype yt, row-major. */
+AR_API ar_status ar_mxfp4_gemm(const void* X, int64_t M, int64_t K, const uint8_t* packed, const uint8_t* scale,
+                        int64_t N, void* Y, ar_dtype yt, void* stream);
+
+/* The same product with packed activations: x_packed [M, K/2], x_scale
+ * [M, K/32].  Products are exact, accumulation is fp32. */
+AR_API ar_status ar_mxfp4_gemm_a4(const uint8_t* x_packed, const uint8_t* x_scale, int64_t M, int64_t K,
+                           const uint8_t* packed, const uint8_t* scale, int64_t N, void* Y, ar_dtype yt,
+                           void* stream);
 
 /* One evaluation of the tuning objective and its straight-through gradients
  * (blog sec. 3 algorithm flow, steps 2-4) on the samples ids[0..B-1] of the

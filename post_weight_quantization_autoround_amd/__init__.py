@@ -97,6 +97,12 @@ def _load() -> ctypes.CDLL:
         "ar_qdq_rtn_noalloc": (st, [P, st, I64, I64, qc, P, P, P, P, st, P, P, P, P]),
         "ar_pack_int4": (st, [P, st, I64, I64, qc, P, P, P, P, P, P, P]),
         "ar_w4a16_gemm": (st, [P, st, I64, I64, P, P, P, I64, I32, P, st, P]),
+        "ar_pack_mxfp4": (st, [P, st, I64, I64, P, P, P, P]),
+        "ar_unpack_mxfp4": (st, [P, P, I64, I64, P, st, P]),
+        "ar_rmsnorm_mxfp4": (st, [P, P, st, F, P, I64, I64, F, P, P, P, P]),
+        "ar_swiglu_mxfp4": (st, [P, I64, P, I64, I64, I64, P, P, P]),
+        "ar_mxfp4_gemm": (st, [P, I64, I64, P, P, I64, P, st, P]),
+        "ar_mxfp4_gemm_a4": (st, [P, P, I64, I64, P, P, I64, P, st, P]),
         "ar_layer_grads": (st, [P, st, I64, I64, P, st, I64, I64, ctypes.POINTER(ctypes.c_int32), I32, qc, st,
                                 P, P, P, ctypes.POINTER(D), P, P, P, P, P]),
         "ar_tune_layer": (st, [P, st, I64, I64, P, st, I64, I64, qc, op, P, P, P,
@@ -256,6 +262,137 @@ def w4a16_gemm(X: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero:
         out = torch.empty((M, N), dtype=out_dtype, device=X.device)
     py = _dev(out, "out", out_dtype, (M, N))
     _check(lib.ar_w4a16_gemm(px, AR_BF16, M, K, pp, ps, pz, N, group_size, py, _dtype_code(out), _stream()))
+    return out
+
+
+# ------------------------------------------------------------ packed MXFP4
+def _mx_in(t, name, dtypes, shape=None, strided=False):
+    """Checks an input of the MXFP4 calls: on the current HIP device, one of
+    `dtypes`, `shape`, contiguous (`strided`: rows may lie apart)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a HIP device, got {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() != 2 and shape is None:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    if strided:
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_F32_BF16 = (torch.float32, torch.bfloat16)
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_U8 = (torch.uint8,)
+
+
+def _mx_out(rows, k, dev):
+    if k % 32 != 0:
+        raise ValueError(f"the last dimension must be a multiple of 32 (the MXFP4 block), got {k}")
+    return (torch.empty((rows, k // 2), dtype=torch.uint8, device=dev),
+            torch.empty((rows, k // 32), dtype=torch.uint8, device=dev))
+
+
+def pack_mxfp4(W: torch.Tensor, alpha: torch.Tensor | None = None):
+    """W [N, K] (fp32 or bf16, K a multiple of 32) as packed MXFP4: returns
+    (packed uint8 [N, K/2], low nibble = even column; scale uint8 [N, K/32],
+    exponent + 127, 255 for a block without a finite maximum).  The codes are
+    those of qdq_rtn(fmt=AR_FMT_MXFP4, bits=4, group_size=32, alpha=alpha);
+    alpha [N, K/32] clips the block maxima."""
+    pw = _mx_in(W, "W", _F32_BF16)
+    N, K = W.shape
+    packed, scale = _mx_out(N, K, W.device)
+    pa = None if alpha is None else _mx_in(alpha, "alpha", _F32, scale.shape)
+    _check(lib.ar_pack_mxfp4(pw, _dtype_code(W), N, K, pa, packed.data_ptr(), scale.data_ptr(), _stream()))
+    return packed, scale
+
+
+def unpack_mxfp4(packed: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.float32):
+    """The values [N, K] of packed MXFP4, fp32 or bf16."""
+    pp = _mx_in(packed, "packed", _U8)
+    N, K = packed.shape[0], 2 * packed.shape[1]
+    ps = _mx_in(scale, "scale", _U8, (N, K // 32))
+    out = torch.empty((N, K), dtype=out_dtype, device=packed.device)
+    _check(lib.ar_unpack_mxfp4(pp, ps, N, K, out.data_ptr(), _dtype_code(out), _stream()))
+    return out
+
+
+def rmsnorm_mxfp4(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-5,
+                  delta: torch.Tensor | None = None, delta_scale: float = 1.0):
+    """h = r / sqrt(mean(r^2) + eps) * weight as packed MXFP4, r = x +
+    delta_scale * delta; x bf16 [M, H], delta bf16 or fp32 [M, H], weight fp32
+    [H] or None (= 1).  Returns (packed, scale, r) with r the bf16 residual
+    stream, None without a delta (r is x then)."""
+    px = _mx_in(x, "x", _BF16)
+    M, H = x.shape
+    pd = None if delta is None else _mx_in(delta, "delta", _F32_BF16, x.shape)
+    pw = None if weight is None else _mx_in(weight, "weight", _F32, (H,))
+    packed, scale = _mx_out(M, H, x.device)
+    r = None if delta is None else torch.empty_like(x)
+    _check(lib.ar_rmsnorm_mxfp4(px, pd, AR_BF16 if delta is None else _dtype_code(delta), delta_scale, pw, M, H, eps,
+                                None if r is None else r.data_ptr(), packed.data_ptr(), scale.data_ptr(), _stream()))
+    return packed, scale, r
+
+
+def swiglu_mxfp4(gate: torch.Tensor, up: torch.Tensor):
+    """silu(gate) * up as packed MXFP4 (packed, scale); gate and up bf16
+    [M, F] with contiguous rows, which may be the halves of one [M, 2F]
+    product (row strides multiples of 8)."""
+    pg = _mx_in(gate, "gate", _BF16, strided=True)
+    pu = _mx_in(up, "up", _BF16, gate.shape, strided=True)
+    M, F = gate.shape
+    packed, scale = _mx_out(M, F, gate.device)
+    # the stride of a lone row means nothing
+    lg, lu = (gate.stride(0), up.stride(0)) if M > 1 else (F, F)
+    _check(lib.ar_swiglu_mxfp4(pg, lg, pu, lu, M, F, packed.data_ptr(), scale.data_ptr(), _stream()))
+    return packed, scale
+
+
+def _mx_y(out, out_dtype, M, N, dev):
+    if out is None:
+        return torch.empty((M, N), dtype=out_dtype, device=dev)
+    _mx_in(out, "out", (out_dtype,), (M, N))
+    return out
+
+
+def mxfp4_gemm(X: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+               out: torch.Tensor | None = None):
+    """Y = X W^T with W the values of pack_mxfp4's output; X bf16 [M, K],
+    packed uint8 [N, K/2], scale uint8 [N, K/32] -> Y [M, N] (fp32 sums, or
+    their bf16 rounding)."""
+    px = _mx_in(X, "X", _BF16)
+    pp = _mx_in(packed, "packed", _U8)
+    (M, K), N = X.shape, packed.shape[0]
+    if 2 * packed.shape[1] != K:
+        raise ValueError(f"X has {K} columns, packed holds {2 * packed.shape[1]}")
+    ps = _mx_in(scale, "scale", _U8, (N, K // 32))
+    out = _mx_y(out, out_dtype, M, N, X.device)
+    _check(lib.ar_mxfp4_gemm(px, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _stream()))
+    return out
+
+
+def mxfp4_gemm_a4(x_packed: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
+                  out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
+    """mxfp4_gemm with activations in packed MXFP4 too (x_packed uint8
+    [M, K/2], x_scale uint8 [M, K/32], as the quantizing calls return them)."""
+    px = _mx_in(x_packed, "x_packed", _U8)
+    pp = _mx_in(packed, "packed", _U8)
+    M, K, N = x_packed.shape[0], 2 * x_packed.shape[1], packed.shape[0]
+    if 2 * packed.shape[1] != K:
+        raise ValueError(f"x_packed holds {K} columns, packed {2 * packed.shape[1]}")
+    pxs = _mx_in(x_scale, "x_scale", _U8, (M, K // 32))
+    ps = _mx_in(scale, "scale", _U8, (N, K // 32))
+    out = _mx_y(out, out_dtype, M, N, x_packed.device)
+    _check(lib.ar_mxfp4_gemm_a4(px, pxs, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _stream()))
     return out
 
 

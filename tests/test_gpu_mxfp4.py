@@ -1,0 +1,425 @@
+"""GPU parity of the packed-MXFP4 operators against the 64-bit oracle.
+
+Codes and scale bytes are compared bit for bit.  Products are compared in two
+ways: on operands whose every partial sum fp32 holds exactly, bit for bit;
+and on general operands within K half-steps of fp32 of sum |x w| (each of at
+most K additions rounds once; the products are exact), plus half a step of
+the output type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mxfp4_ref as mx
+from synthetic_inputs import make_weight, to_bf16_values
+
+pytestmark = pytest.mark.gpu
+F32 = np.float32
+U24 = 2.0 ** -24          # half a step of fp32, relative
+U8 = 2.0 ** -8            # half a step of bf16, relative
+
+
+@pytest.fixture(scope="module")
+def ar():
+    import post_weight_quantization_autoround_amd as mod
+    assert torch.cuda.is_available()
+    return mod
+
+
+def _dev(a, bf16=False):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t.to(torch.bfloat16) if bf16 else t
+
+
+def _np(t):
+    return t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+
+
+def _same_packed(got, codes, scale, what=""):
+    packed, sc = (t.cpu().numpy() for t in got[:2])
+    np.testing.assert_array_equal(sc, scale, err_msg=what)
+    np.testing.assert_array_equal(mx.unpack(packed), codes, err_msg=what)
+
+
+def _hard_weight(rng, n, k):
+    """A weight with blocks of zeros, ties, NaN, infinities and magnitudes from the smallest to the largest."""
+    W = make_weight(rng, n, k)
+    W[0] = 0.0
+    if n > 1:
+        W[1] = np.resize(F32([10, 0.5, -1.5, -0.1, 7, 5, -3.5, 2.5, -0.0, 0.25, 1.25, 1.75, 8, 12, -12]), k)
+    if n > 3:
+        W[2] *= F32(2.0 ** -126)
+        W[3] *= F32(2.0 ** 120)
+    if n > 6:
+        W[4, 5], W[5, k - 1], W[6, 0] = np.nan, np.inf, -np.inf
+    if n > 8:
+        W[7], W[8] = F32(1e-45), F32(3.4e38)
+    return W
+
+
+# ------------------------------------------------------------ pack, unpack
+@pytest.mark.parametrize("n,k", [(1, 32), (3, 96), (17, 64), (64, 2080), (5, 11008)])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("clip", [False, True])
+def test_pack_and_unpack(ar, n, k, bf16, clip):
+    rng = np.random.default_rng(n + k)
+    W = _hard_weight(rng, max(n, 9), k)[-n:] if n < 9 else _hard_weight(rng, n, k)
+    W = to_bf16_values(W) if bf16 else W
+    alpha = rng.uniform(0.5, 1.0, (n, k // 32)).astype(F32) if clip else None
+    if clip and n > 16:
+        alpha[16, 0], alpha[15, 0] = 0.0, np.nan
+    codes, scale = mx.quantize(W, alpha)
+    got = ar.pack_mxfp4(_dev(W, bf16), alpha=None if alpha is None else _dev(alpha))
+    _same_packed(got, codes, scale)
+    with np.errstate(over="ignore"):
+        want = mx.values(mx.pack(codes), scale).astype(F32)
+    for dt in (torch.float32, torch.bfloat16):
+        v = _np(ar.unpack_mxfp4(*got, out_dtype=dt))
+        np.testing.assert_array_equal(v, want)      # every value is exact in either type
+
+
+def test_unpack_every_code_and_scale(ar):
+    packed = np.resize(np.arange(256, dtype=np.uint8), (256, 256))
+    scale = np.repeat(np.arange(256, dtype=np.uint8)[:, None], 16, axis=1)
+    with np.errstate(over="ignore"):
+        want = mx.values(packed, scale).astype(F32)     # 2^126 * 4 and above: infinite in fp32
+    for dt in (torch.float32, torch.bfloat16):
+        np.testing.assert_array_equal(_np(ar.unpack_mxfp4(_dev(packed), _dev(scale), out_dtype=dt)), want)
+
+
+@pytest.mark.parametrize("clip", [False, True])
+def test_pack_equals_the_tensor_level_quantizer(ar, clip):
+    rng = np.random.default_rng(5)
+    W = _dev(make_weight(rng, 128, 1024), bf16=True)
+    alpha = _dev(rng.uniform(0.5, 1.0, (128, 32)).astype(F32)) if clip else None
+    q = ar.qdq_rtn(W, bits=4, group_size=32, alpha=alpha, fmt=ar.AR_FMT_MXFP4)
+    packed, scale = ar.pack_mxfp4(W, alpha=alpha)
+    codes = torch.stack((packed & 15, packed >> 4), -1).reshape(128, 1024)
+    assert torch.equal(codes, q["codes"]) and torch.equal(scale, q["zero"])
+    assert torch.equal(ar.unpack_mxfp4(packed, scale), q["w_hat"])
+
+
+def test_pack_past_32_bit_offsets(ar):
+    n, k = 270_000, 16_384                    # 4.4 Gi elements, 8.8 GB of bf16
+    W = torch.zeros((n, k), dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(6)
+    rows = [0, 131_071, 131_072, 262_143, 262_144, n - 1]
+    part = to_bf16_values(make_weight(rng, len(rows), k))
+    W[rows] = _dev(part, bf16=True)
+    packed, scale = ar.pack_mxfp4(W)
+    codes, sc = mx.quantize(part)
+    _same_packed((packed[rows], scale[rows]), codes, sc)
+    assert int(packed.count_nonzero()) == int(packed[rows].count_nonzero())
+    back = ar.unpack_mxfp4(packed, scale, out_dtype=torch.bfloat16)
+    np.testing.assert_array_equal(_np(back[rows]), mx.values(mx.pack(codes), sc).astype(F32))
+
+
+# --------------------------------------------------------------- RMS norm
+@pytest.mark.parametrize("m,h", [(1, 32), (1, 4096), (3, 96), (5, 2080), (2, 8192), (3, 11008), (2, 20000), (1, 32768)])
+@pytest.mark.parametrize("delta", ["none", "bf16", "f32"])
+def test_rmsnorm(ar, m, h, delta):
+    h = h // 32 * 32
+    rng = np.random.default_rng(m + h)
+    x = to_bf16_values((rng.standard_normal((m, h)) * rng.uniform(0.1, 30, (m, 1))).astype(F32))
+    x[:, :2] *= 64
+    d = None if delta == "none" else rng.standard_normal((m, h)).astype(F32)
+    d = to_bf16_values(d) if delta == "bf16" else d
+    w = (1 + 0.2 * rng.standard_normal(h)).astype(F32) if h % 64 == 0 else None
+    c = 0.3
+    r = mx.residual(x, d, c)
+    codes, scale = mx.quantize(mx.rmsnorm(r, w, 1e-5))
+    got = ar.rmsnorm_mxfp4(_dev(x, True), weight=None if w is None else _dev(w), eps=1e-5,
+                           delta=None if d is None else _dev(d, delta == "bf16"), delta_scale=c)
+    _same_packed(got, codes, scale)
+    if d is None:
+        assert got[2] is None
+    else:
+        np.testing.assert_array_equal(_np(got[2]), to_bf16_values(r))
+
+
+def test_rmsnorm_hard_rows(ar):
+    # rows of zeros (also with eps = 0: 0 / 0), of one value whose norm is 1 (exact ties with the weight),
+    # with NaN, an infinity, with magnitudes that under- and overflow in fp32
+    h = 128
+    x = np.zeros((9, h), F32)
+    x[1] = 3.0
+    x[2] = np.resize(F32([1.0, -1.0]), h)
+    x[3], x[3, 7] = 1.0, np.nan
+    x[4], x[4, 40] = 1.0, np.inf
+    x[5] = 2.0 ** -130
+    x[6], x[6, 64] = 2.0 ** -120, 2.0 ** 100
+    x[7] = 2.0 ** 127
+    x[8, :32] = 1.0
+    w = np.resize(F32([2.5, 0.25, 5, -0.75, 1, 3.5, 0, 1e30, 1e-30]), h)
+    x = to_bf16_values(x)
+    for eps in (0.0, 1e-5):
+        for ww in (None, w):
+            codes, scale = mx.quantize(mx.rmsnorm(x, ww, eps))
+            got = ar.rmsnorm_mxfp4(_dev(x, True), weight=None if ww is None else _dev(ww), eps=eps)
+            _same_packed(got, codes, scale, f"eps {eps} weight {ww is not None}")
+
+
+# ----------------------------------------------------------------- SwiGLU
+@pytest.mark.parametrize("m,f,joined", [(1, 32, False), (1, 11008, True), (7, 96, True), (33, 2080, False),
+                                        (130, 1024, True)])
+def test_swiglu(ar, m, f, joined):
+    rng = np.random.default_rng(m * f)
+    g = to_bf16_values((rng.standard_normal((m, f)) * 4).astype(F32))
+    u = to_bf16_values(rng.standard_normal((m, f)).astype(F32))
+    if joined:
+        both = _dev(np.concatenate([g, u], axis=1), True)
+        gate, up = both[:, :f], both[:, f:]
+    else:
+        gate, up = _dev(g, True), _dev(u, True)
+    codes, scale = mx.quantize(mx.swiglu(g, u))
+    _same_packed(ar.swiglu_mxfp4(gate, up), codes, scale)
+
+
+def test_swiglu_hard_values(ar):
+    # every finite bf16 gate with factors that give ties, tiny and huge products; NaN and infinities
+    bits = np.arange(1 << 16, dtype=np.uint32) << 16
+    g = bits.view(F32).reshape(-1, 32)
+    g = np.where(np.isfinite(g), g, F32(0.5)).astype(F32)
+    for factor in (1.0, 2.5, 2.0 ** -130, 2.0 ** 100, 0.0):
+        u = np.full_like(g, to_bf16_values(F32([factor]))[0])
+        codes, scale = mx.quantize(mx.swiglu(g, u))
+        _same_packed(ar.swiglu_mxfp4(_dev(g, True), _dev(u, True)), codes, scale, f"factor {factor}")
+    g = np.ones((6, 64), F32)
+    u = np.ones((6, 64), F32)
+    g[0, 3], g[1, 4], g[2, 5], u[3, 6], u[4, 40] = np.nan, np.inf, -np.inf, np.nan, -np.inf
+    g[5], u[5, 3] = -100.0, np.inf
+    codes, scale = mx.quantize(mx.swiglu(g, u))
+    _same_packed(ar.swiglu_mxfp4(_dev(g, True), _dev(u, True)), codes, scale, "nonfinite")
+
+
+# --------------------------------------------------------------- products
+SHAPES = [(1, 1, 32), (1, 16, 64), (1, 4096, 4096), (2, 33, 96), (3, 100, 160), (15, 17, 128), (16, 256, 2048),
+          (17, 129, 288), (31, 64, 512), (32, 1000, 2080), (33, 96, 4096), (64, 130, 256), (65, 48, 1120),
+          (100, 300, 736), (130, 520, 1056), (256, 256, 512), (257, 511, 544), (300, 1030, 416), (513, 260, 2304),
+          (700, 40, 64), (1, 30000, 96), (40, 24, 32768)]
+
+
+def _exact_operand(rng, rows, k):
+    """Packed operand whose values are multiples of 2^-2 of magnitude at most 12: with one like it, products are
+    multiples of 2^-4 of at most 144, and K < 2^24 / (16 * 144) = 7281 of them sum exactly in fp32 in any order.  Larger
+    K have the scale 2^-1 alone: products of at most 9, K < 2^24 / (16 * 9) = 116508."""
+    codes = rng.integers(0, 16, (rows, k)).astype(np.uint8)
+    codes[codes == 8] = 0
+    if k > 7000:
+        return mx.pack(codes), np.full((rows, k // 32), 126, np.uint8)
+    return mx.pack(codes), rng.integers(126, 129, (rows, k // 32)).astype(np.uint8)
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_products_exact(ar, m, n, k):
+    rng = np.random.default_rng(m + 3 * n + 7 * k)
+    wp, ws = _exact_operand(rng, n, k)
+    xp, xs = _exact_operand(rng, m, k)
+    X, W = mx.values(xp, xs), mx.values(wp, ws)
+    ref = (X @ W.T).astype(F32)
+    x16 = _dev(X.astype(F32), True)
+    for dt in (torch.float32, torch.bfloat16):
+        want = ref if dt == torch.float32 else to_bf16_values(ref)
+        print(f"a16 {m}x{n}x{k} {dt}", flush=True)
+        np.testing.assert_array_equal(_np(ar.mxfp4_gemm(x16, _dev(wp), _dev(ws), out_dtype=dt)), want)
+        print(f"a4 {m}x{n}x{k} {dt}", flush=True)
+        np.testing.assert_array_equal(_np(ar.mxfp4_gemm_a4(_dev(xp), _dev(xs), _dev(wp), _dev(ws), out_dtype=dt)), want)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 520, 4096), (16, 300, 11008), (40, 257, 2080), (130, 512, 4096),
+                                   (520, 300, 1056)])
+def test_products_general(ar, m, n, k):
+    rng = np.random.default_rng(m + n + k)
+    W = make_weight(rng, n, k)
+    W[:, :32] *= F32(2.0 ** 20)
+    X = to_bf16_values(rng.standard_normal((m, k)).astype(F32))
+    X[0] *= F32(2.0 ** -30)
+    wp, ws = ar.pack_mxfp4(_dev(W))
+    xp, xs = ar.pack_mxfp4(_dev(X, True))
+    Wv = mx.values(wp.cpu().numpy(), ws.cpu().numpy())
+    for Xv, call in ((X, lambda dt: ar.mxfp4_gemm(_dev(X, True), wp, ws, out_dtype=dt)),
+                     (mx.values(xp.cpu().numpy(), xs.cpu().numpy()),
+                      lambda dt: ar.mxfp4_gemm_a4(xp, xs, wp, ws, out_dtype=dt))):
+        ref, mag = mx.product(Xv, Wv)
+        tol = k * U24 * mag
+        err = np.abs(_np(call(torch.float32)).astype(np.float64) - ref)
+        assert (err <= tol).all(), (err / mag).max()
+        err = np.abs(_np(call(torch.bfloat16)).astype(np.float64) - ref)
+        assert (err <= tol + U8 * (np.abs(ref) + tol)).all()
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 130, 600])
+def test_products_write_their_output_only(ar, m):
+    n, k = 261, 160
+    rng = np.random.default_rng(m)
+    wp, ws = _exact_operand(rng, n, k)
+    xp, xs = _exact_operand(rng, m, k)
+    X, W = mx.values(xp, xs), mx.values(wp, ws)
+    ref = (X @ W.T).astype(F32)
+    for a4 in (False, True):
+        buf = torch.full((m + 2, n), 7.0, device="cuda")
+        out = buf[1:m + 1]
+        if a4:
+            ar.mxfp4_gemm_a4(_dev(xp), _dev(xs), _dev(wp), _dev(ws), out=out)
+        else:
+            ar.mxfp4_gemm(_dev(X.astype(F32), True), _dev(wp), _dev(ws), out=out)
+        got = _np(buf)
+        np.testing.assert_array_equal(got[1:-1], ref)
+        assert (got[0] == 7).all() and (got[-1] == 7).all()
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 300])
+def test_products_carry_nan_and_infinity(ar, m):
+    # a NaN block of the weight spoils its output column, a NaN or infinite activation its row, and nothing else
+    n, k = 140, 320
+    rng = np.random.default_rng(m)
+    wp, ws = _exact_operand(rng, n, k)
+    xp, xs = _exact_operand(rng, m, k)
+    X = mx.values(xp, xs)
+    W = mx.values(wp, ws)
+    ref = (X @ W.T).astype(F32)
+    ws2, xs2, X2 = ws.copy(), xs.copy(), X.copy()
+    ws2[77, 9] = 255
+    xs2[m - 1, 3] = 255
+    X2[m - 1, 100] = np.nan
+    ref2 = ref.copy()
+    ref2[m - 1] = np.nan
+    ref2[:, 77] = np.nan
+    for dt in (torch.float32, torch.bfloat16):
+        want = ref2 if dt == torch.float32 else to_bf16_values(ref2)
+        np.testing.assert_array_equal(
+            _np(ar.mxfp4_gemm(_dev(X2.astype(F32), True), _dev(wp), _dev(ws2), out_dtype=dt)), want)
+        np.testing.assert_array_equal(
+            _np(ar.mxfp4_gemm_a4(_dev(xp), _dev(xs2), _dev(wp), _dev(ws2), out_dtype=dt)), want)
+
+
+def test_products_past_32_bit_offsets(ar):
+    # Y of 4.5 G elements (18 GB of fp32): rows past element 2^32 against the first ones
+    m, n, k = 140_000, 32_000, 32
+    rng = np.random.default_rng(9)
+    wp, ws = _exact_operand(rng, n, k)
+    xp, xs = _exact_operand(rng, 1000, k)
+    ref = (mx.values(xp, xs) @ mx.values(wp, ws).T).astype(F32)
+    xpd, xsd = _dev(xp).repeat(m // 1000, 1), _dev(xs).repeat(m // 1000, 1)
+    want = _dev(ref)
+    for a4 in (False, True):
+        if a4:
+            Y = ar.mxfp4_gemm_a4(xpd, xsd, _dev(wp), _dev(ws))
+        else:
+            Y = ar.mxfp4_gemm(ar.unpack_mxfp4(xpd, xsd, out_dtype=torch.bfloat16), _dev(wp), _dev(ws))
+        for first in (0, 67_000, 134_000, m - 1000):
+            assert torch.equal(Y[first:first + 1000], want), first
+        del Y
+
+
+# ------------------------------------------------- together, as they are used
+def _mlp(ar, s, x, delta):
+    """The MLP of a decoder block on packed weights and activations: norm with residual, gate and up as one product,
+    SwiGLU, down projection."""
+    hp, hs, r = ar.rmsnorm_mxfp4(x, weight=s["norm"], delta=delta)
+    gu = ar.mxfp4_gemm_a4(hp, hs, *s["gate_up"], out_dtype=torch.bfloat16)
+    f = gu.shape[1] // 2
+    ap, as_ = ar.swiglu_mxfp4(gu[:, :f], gu[:, f:])
+    return ar.mxfp4_gemm_a4(ap, as_, *s["down"]), r, gu, (hp, hs), (ap, as_)
+
+
+@pytest.mark.parametrize("m", [1, 37, 300])
+def test_mlp_of_packed_operators(ar, m):
+    H, F = 256, 704
+    rng = np.random.default_rng(m)
+    gu_w, down_w = make_weight(rng, 2 * F, H), make_weight(rng, H, F)
+    norm = (1 + 0.1 * rng.standard_normal(H)).astype(F32)
+    s = dict(norm=_dev(norm), gate_up=ar.pack_mxfp4(_dev(gu_w, True)), down=ar.pack_mxfp4(_dev(down_w, True)))
+    x = to_bf16_values(rng.standard_normal((m, H)).astype(F32))
+    d = rng.standard_normal((m, H)).astype(F32)
+    y, r, gu, hq, aq = _mlp(ar, s, _dev(x, True), _dev(d))
+    rr = mx.residual(x, d, 1.0)
+    np.testing.assert_array_equal(_np(r), to_bf16_values(rr))
+    codes, scale = mx.quantize(mx.rmsnorm(rr, norm, 1e-5))
+    _same_packed(hq, codes, scale)
+    W1 = mx.values(*(t.cpu().numpy() for t in s["gate_up"]))
+    ref, mag = mx.product(mx.values(mx.pack(codes), scale), W1)
+    tol = H * U24 * mag
+    assert (np.abs(_np(gu) - ref) <= tol + U8 * (np.abs(ref) + tol)).all()
+    g = _np(gu)                                              # from here on the GPU's own bf16 product
+    codes, scale = mx.quantize(mx.swiglu(g[:, :F], g[:, F:]))
+    _same_packed(aq, codes, scale)
+    ref, mag = mx.product(mx.values(mx.pack(codes), scale), mx.values(*(t.cpu().numpy() for t in s["down"])))
+    assert (np.abs(_np(y) - ref) <= F * U24 * mag).all()
+
+
+@pytest.mark.parametrize("m", [1, 16, 130])
+def test_captured_graph_and_other_streams(ar, m):
+    # the chain captured once and replayed with new inputs in place, eager work between the replays; then two
+    # streams at once
+    H, F = 256, 704
+    rng = np.random.default_rng(100 + m)
+    s = dict(norm=_dev(np.ones(H, F32)), gate_up=ar.pack_mxfp4(_dev(make_weight(rng, 2 * F, H))),
+             down=ar.pack_mxfp4(_dev(make_weight(rng, H, F))))
+    x = _dev(rng.standard_normal((m, H)).astype(F32), True)
+    d = _dev(rng.standard_normal((m, H)).astype(F32))
+
+    def both():
+        y, r = _mlp(ar, s, x, d)[:2]
+        return y, r, ar.mxfp4_gemm(r, *s["gate_up"]), ar.unpack_mxfp4(*s["down"])
+
+    both()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = both()
+    torch.cuda.synchronize()
+    for rep in range(4):
+        x.copy_(_dev(rng.standard_normal((m, H)).astype(F32), True))
+        d.mul_(-0.7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = both()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), rep
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(both())
+    torch.cuda.synchronize()
+    for o in outs:
+        for a, b in zip(o, want):
+            assert torch.equal(a, b)
+    del graph
+
+
+def test_binding_refusals(ar):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    p, s = ar.pack_mxfp4(x)
+    for call, err in [
+        (lambda: ar.pack_mxfp4(x[:, :48].contiguous()), ValueError),
+        (lambda: ar.pack_mxfp4(x.half()), TypeError),
+        (lambda: ar.pack_mxfp4(x.t()), ValueError),
+        (lambda: ar.pack_mxfp4(x[0]), ValueError),
+        (lambda: ar.pack_mxfp4(x, alpha=torch.ones(4, 3, device="cuda")), ValueError),
+        (lambda: ar.unpack_mxfp4(p, s[:, :1].contiguous()), ValueError),
+        (lambda: ar.unpack_mxfp4(p, s, out_dtype=torch.float16), TypeError),
+        (lambda: ar.rmsnorm_mxfp4(x, weight=torch.ones(32, device="cuda")), ValueError),
+        (lambda: ar.rmsnorm_mxfp4(x, delta=x[:2]), ValueError),
+        (lambda: ar.swiglu_mxfp4(x, x[:, :32]), ValueError),
+        (lambda: ar.swiglu_mxfp4(x.t(), x.t()), ValueError),
+        (lambda: ar.swiglu_mxfp4(x[:, 4:36], x[:, 4:36]), ar.ARError),      # not 16-byte aligned
+        (lambda: ar.mxfp4_gemm(x[:, :32].contiguous(), p, s), ValueError),
+        (lambda: ar.mxfp4_gemm(x, p, s, out=torch.empty(4, 5, device="cuda")), ValueError),
+        (lambda: ar.mxfp4_gemm(x, p, s, out_dtype=torch.bfloat16, out=torch.empty(4, 4, device="cuda")), TypeError),
+        (lambda: ar.mxfp4_gemm_a4(p, s, p[:, :16].contiguous(), s), ValueError),
+        (lambda: ar.mxfp4_gemm_a4(p, s[:2], p, s), ValueError),
+    ]:
+        with pytest.raises(err):
+            call()
+    e = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    ep, es = ar.pack_mxfp4(e)
+    assert ep.shape == (0, 32) and es.shape == (0, 2)
+    assert ar.unpack_mxfp4(ep, es).shape == (0, 64)
+    assert ar.mxfp4_gemm(e, p, s).shape == (0, 4) and ar.mxfp4_gemm_a4(ep, es, p, s).shape == (0, 4)
+    assert ar.swiglu_mxfp4(e, e)[0].shape == (0, 32) and ar.rmsnorm_mxfp4(e)[0].shape == (0, 32)

@@ -1,0 +1,97 @@
+"""Refusals of the packed-MXFP4 entry points: checked on the host before any
+HIP call, so these run without a GPU."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "post_weight_quantization_autoround_amd", "libautoround.so")
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libautoround.so not built")
+
+P = ctypes.c_void_p(0x1000)       # never dereferenced: checks fail first
+ODD = ctypes.c_void_p(0x1004)     # not 16-byte aligned
+
+
+@pytest.fixture(scope="module")
+def ar():
+    import post_weight_quantization_autoround_amd as mod
+    return mod
+
+
+def _call(ar, name, **kw):
+    order = {
+        "ar_pack_mxfp4": dict(W=P, wt=1, N=4, K=64, alpha=None, packed=P, scale=P, stream=None),
+        "ar_unpack_mxfp4": dict(packed=P, scale=P, N=4, K=64, W=P, wt=1, stream=None),
+        "ar_rmsnorm_mxfp4": dict(x=P, delta=None, dt=1, c=1.0, w=None, M=4, H=64, eps=1e-5, r=None, packed=P, scale=P,
+                                 stream=None),
+        "ar_swiglu_mxfp4": dict(gate=P, ldg=64, up=P, ldu=64, M=4, F=64, packed=P, scale=P, stream=None),
+        "ar_mxfp4_gemm": dict(X=P, M=4, K=64, packed=P, scale=P, N=8, Y=P, yt=0, stream=None),
+        "ar_mxfp4_gemm_a4": dict(xp=P, xs=P, M=4, K=64, packed=P, scale=P, N=8, Y=P, yt=0, stream=None),
+    }[name]
+    assert set(kw) <= set(order)
+    order.update(kw)
+    return getattr(ar.lib, name)(*order.values())
+
+
+INVALID, UNSUPPORTED = 1, 2
+CASES = [
+    ("ar_pack_mxfp4", dict(W=None), INVALID), ("ar_pack_mxfp4", dict(packed=None), INVALID),
+    ("ar_pack_mxfp4", dict(scale=None), INVALID), ("ar_pack_mxfp4", dict(N=-1), INVALID),
+    ("ar_pack_mxfp4", dict(K=0), INVALID), ("ar_pack_mxfp4", dict(K=48), INVALID),
+    ("ar_pack_mxfp4", dict(wt=7), INVALID), ("ar_pack_mxfp4", dict(W=ODD), UNSUPPORTED),
+    ("ar_pack_mxfp4", dict(packed=ODD), UNSUPPORTED), ("ar_pack_mxfp4", dict(N=1 << 40), UNSUPPORTED),
+    ("ar_pack_mxfp4", dict(K=1 << 30), UNSUPPORTED),
+    ("ar_unpack_mxfp4", dict(W=None), INVALID), ("ar_unpack_mxfp4", dict(K=40), INVALID),
+    ("ar_unpack_mxfp4", dict(wt=-1), INVALID), ("ar_unpack_mxfp4", dict(packed=ODD), UNSUPPORTED),
+    ("ar_unpack_mxfp4", dict(scale=None), INVALID),
+    ("ar_rmsnorm_mxfp4", dict(x=None), INVALID), ("ar_rmsnorm_mxfp4", dict(H=100), INVALID),
+    ("ar_rmsnorm_mxfp4", dict(eps=-1.0), INVALID), ("ar_rmsnorm_mxfp4", dict(eps=float("nan")), INVALID),
+    ("ar_rmsnorm_mxfp4", dict(delta=P, dt=5), INVALID), ("ar_rmsnorm_mxfp4", dict(H=32800), UNSUPPORTED),
+    ("ar_rmsnorm_mxfp4", dict(w=ODD), UNSUPPORTED), ("ar_rmsnorm_mxfp4", dict(delta=ODD), UNSUPPORTED),
+    ("ar_rmsnorm_mxfp4", dict(r=ODD), UNSUPPORTED), ("ar_rmsnorm_mxfp4", dict(M=-2), INVALID),
+    ("ar_swiglu_mxfp4", dict(gate=None), INVALID), ("ar_swiglu_mxfp4", dict(up=None), INVALID),
+    ("ar_swiglu_mxfp4", dict(ldg=63), INVALID), ("ar_swiglu_mxfp4", dict(ldu=32), INVALID),
+    ("ar_swiglu_mxfp4", dict(ldu=68), UNSUPPORTED), ("ar_swiglu_mxfp4", dict(up=ODD), UNSUPPORTED),
+    ("ar_swiglu_mxfp4", dict(F=8), INVALID),
+    ("ar_mxfp4_gemm", dict(X=None), INVALID), ("ar_mxfp4_gemm", dict(Y=None), INVALID),
+    ("ar_mxfp4_gemm", dict(packed=None), INVALID), ("ar_mxfp4_gemm", dict(scale=None), INVALID),
+    ("ar_mxfp4_gemm", dict(N=0), INVALID), ("ar_mxfp4_gemm", dict(M=-1), INVALID),
+    ("ar_mxfp4_gemm", dict(K=80), INVALID), ("ar_mxfp4_gemm", dict(yt=2), INVALID),
+    ("ar_mxfp4_gemm", dict(X=ODD), UNSUPPORTED), ("ar_mxfp4_gemm", dict(packed=ODD), UNSUPPORTED),
+    ("ar_mxfp4_gemm", dict(M=1 << 30, K=32), UNSUPPORTED),
+    ("ar_mxfp4_gemm", dict(M=1 << 21, N=1 << 20), UNSUPPORTED), ("ar_mxfp4_gemm", dict(M=0, K=33), INVALID),
+    ("ar_mxfp4_gemm_a4", dict(xp=None), INVALID), ("ar_mxfp4_gemm_a4", dict(xs=None), INVALID),
+    ("ar_mxfp4_gemm_a4", dict(Y=None), INVALID), ("ar_mxfp4_gemm_a4", dict(xp=ODD), UNSUPPORTED),
+    ("ar_mxfp4_gemm_a4", dict(K=16), INVALID), ("ar_mxfp4_gemm_a4", dict(N=-3), INVALID),
+]
+
+
+@pytest.mark.parametrize("name,kw,expect", CASES)
+def test_refused(ar, name, kw, expect):
+    assert _call(ar, name, **kw) == expect
+    assert ar.lib.ar_last_error().decode()
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("ar_pack_mxfp4", dict(N=0, W=None, packed=None, scale=None)),
+    ("ar_unpack_mxfp4", dict(N=0, W=None, packed=None, scale=None)),
+    ("ar_rmsnorm_mxfp4", dict(M=0, x=None, packed=None, scale=None)),
+    ("ar_swiglu_mxfp4", dict(M=0, gate=None, up=None, packed=None, scale=None)),
+    ("ar_mxfp4_gemm", dict(M=0, X=None, Y=None)),
+    ("ar_mxfp4_gemm_a4", dict(M=0, xp=None, xs=None, Y=None)),
+])
+def test_no_rows_is_an_empty_problem(ar, name, kw):
+    assert _call(ar, name, **kw) == 0
+
+
+def test_binding_refuses_host_tensors(ar):
+    w = torch.zeros(4, 64, dtype=torch.bfloat16)
+    u = torch.zeros(4, 32, dtype=torch.uint8)
+    for call in (lambda: ar.pack_mxfp4(w), lambda: ar.unpack_mxfp4(u, u), lambda: ar.rmsnorm_mxfp4(w),
+                 lambda: ar.swiglu_mxfp4(w, w), lambda: ar.mxfp4_gemm(w, u, u), lambda: ar.mxfp4_gemm_a4(u, u, u, u)):
+        with pytest.raises(ValueError, match="HIP device"):
+            call()
+    with pytest.raises(TypeError):
+        ar.pack_mxfp4([1.0])
