@@ -214,8 +214,9 @@ AR_API ar_status ar_w4a16_gemm(const void* X, ar_dtype xt, int64_t M, int64_t K,
  * The six calls below allocate nothing, so they may be captured into a HIP
  * graph, and are stream-ordered without synchronization.  Common errors:
  * AR_ERR_INVALID_ARG for a NULL pointer, negative rows or a K that is no
- * positive multiple of 32; AR_ERR_UNSUPPORTED for K >= 2^30, more than 2^34
- * elements (2^40 of Y) or a pointer that is not 16-byte aligned (scales and Y: any).
+ * positive multiple of 32; AR_ERR_UNSUPPORTED for K >= 2^30 (products:
+ * 2^23), more than 2^34 elements (2^40 of Y) or a pointer that is not 16-byte
+ * aligned (scales and Y: any).
  * Outputs must not overlap inputs. */
 
 /* Quantize W DEVICE [N, K] (fp32 or bf16) to packed MXFP4: the codes of

@@ -46,12 +46,14 @@ struct MxGateArgs {
 };
 hipError_t launch_mx_swiglu(const MxGateArgs& a, hipStream_t stream);
 
+constexpr int64_t kMxGemmMaxK = 1 << 23;   // 256 rows of bf16 X within 32-bit byte offsets
+
 // Y[m, n] = sum_k X[m, k] W[n, k], W packed; X bf16 (x) or packed (xp, xs).
 struct MxGemmArgs {
     const uint16_t* x;                         // bf16 [M, K], or
     const uint8_t* xp; const uint8_t* xs;      // [M, K/2], [M, K/32]
     const uint8_t* wp; const uint8_t* ws;      // [N, K/2], [N, K/32]
-    int64_t M, N, K;                           // K a multiple of 32
+    int64_t M, N, K;                           // K a multiple of 32, below kMxGemmMaxK
     void* y; bool y_bf16;                      // [M, N]
 };
 hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream);

@@ -35,6 +35,7 @@ ar_status check_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* packed, con
     if (st != AR_OK) return st;
     // at most 2^34 / 32 rows on either side: the product of the two cannot overflow
     if (M * N > (int64_t)1 << 40) return fail(AR_ERR_UNSUPPORTED, "Y may hold at most 2^40 elements");
+    if (K >= kMxGemmMaxK) return fail(AR_ERR_UNSUPPORTED, "the products need K below %lld", (long long)kMxGemmMaxK);
     if (!packed || !scale) return fail(AR_ERR_INVALID_ARG, "packed and scale must be non-NULL");
     if (!dtype_ok(yt)) return fail(AR_ERR_INVALID_ARG, "unknown output dtype");
     if (!aligned(packed, 16)) return fail(AR_ERR_UNSUPPORTED, "packed must be 16-byte aligned");

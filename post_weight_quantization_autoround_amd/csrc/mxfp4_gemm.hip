@@ -3,28 +3,31 @@
 // bf16, so the bf16-activation form multiplies the unpacked weight itself;
 // the packed-activation form feeds both operands' codes and scale bytes to
 // the scaled MFMA, which multiplies their values exactly.
+//
+// K is a multiple of 32, so a 16-byte piece of packed codes is one block.
+#include <type_traits>
+
 #include "ar_internal.h"
+#include "gemm_tiles.h"
 #include "mxfp4.h"
 
 namespace ar {
 namespace {
 
+using gemm::gbl_void;
+using gemm::lds_barrier;
+using gemm::lds_void;
+using gemm::wait_vmcnt;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 template <bool BF16>
 __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
-    if constexpr (BF16) static_cast<uint16_t*>(y)[i] = f32_to_bf16(v);
+    if constexpr (BF16) static_cast<uint16_t*>(y)[i] = (uint16_t)pack_bf16x2(v, v);
     else static_cast<float*>(y)[i] = v;
-}
-
-// f32_to_bf16 of a NaN may carry into infinity; keep it a NaN.
-template <bool BF16>
-__device__ __forceinline__ void store_acc(void* y, int64_t i, float v) {
-    if (BF16 && v != v) static_cast<uint16_t*>(y)[i] = 0x7FC0;
-    else store_y<BF16>(y, i, v);
 }
 
 __device__ __forceinline__ bf16x8 unpack8(uint32_t p, float s) {
@@ -35,67 +38,491 @@ __device__ __forceinline__ bf16x8 unpack8(uint32_t p, float s) {
     o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(p, s, 3));
     return __builtin_bit_cast(bf16x8, o);
 }
+__device__ __forceinline__ float scale_f32(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// A wavefront computes 32 x 32 outputs straight from global memory.  Rows
-// past M or N are clamped; their results are not stored.
-template <bool A4, bool BF16>
-__global__ void __launch_bounds__(256) mx_gemm_direct_kernel(MxGemmArgs a) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 31, half = lane >> 5;
-    const int64_t tiles_n = (a.N + 127) / 128, tile_m = blockIdx.x / tiles_n;
-    const int64_t n0 = ((blockIdx.x - tile_m * tiles_n) * 4 + wave) * 32, m0 = tile_m * 32;
-    if (n0 >= a.N) return;
-    const int64_t m = m0 + r < a.M ? m0 + r : a.M - 1, n = n0 + r < a.N ? n0 + r : a.N - 1;
-    const uint8_t* wrow = a.wp + n * (a.K / 2);
-    const uint8_t* wsc = a.ws + n * (a.K / 32);
-    f32x16 acc = {};
-    if constexpr (A4) {
-        const uint8_t* xrow = a.xp + m * (a.K / 2);
-        const uint8_t* xsc = a.xs + m * (a.K / 32);
-        for (int64_t b = half; b < (a.K / 32 + 1) / 2 * 2; b += 2) {   // block b of the rows; past the end: zeros
-            i32x8 av = {}, wv = {};
-            int as = 0, ws = 0;
-            if (b < a.K / 32) {
-                const u32x4 p = *reinterpret_cast<const u32x4*>(xrow + b * 16);
-                const u32x4 q = *reinterpret_cast<const u32x4*>(wrow + b * 16);
+// The fp4 operand of the scaled MFMA is the low half of its eight registers.
+__device__ __forceinline__ i32x8 fp4_operand(u32x4 v) {
+    i32x8 o;   // the high half is not read
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    av[i] = (int)p[i];
-                    wv[i] = (int)q[i];
-                }
-                as = xsc[b];
-                ws = wsc[b];
-            }
-            acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, wv, acc, 4, 4, 0, as, 0, ws);
-        }
-    } else {
-        const uint16_t* xrow = a.x + m * a.K;
-        for (int64_t k = half * 8; k < a.K; k += 16) {
-            const bf16x8 av = *reinterpret_cast<const bf16x8*>(xrow + k);
-            const uint32_t p = *reinterpret_cast<const uint32_t*>(wrow + k / 2);
-            const bf16x8 wv = unpack8(p, __uint_as_float((uint32_t)wsc[k / 32] << 23));
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, wv, acc, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) o[i] = (int)v[i];
+    return o;
+}
+
+constexpr int64_t kMxTileMaxN = 1 << 22;   // 256 rows of fp32 Y within 32-bit byte offsets
+
+// Tile of workgroup blockIdx.x among tiles_m x tiles_n.  Workgroup b runs on
+// XCD b % 8, each with its own L2: an XCD gets one contiguous run of the tile
+// order, which walks bands of up to 4 tile rows column by column, so the
+// tiles it works on at a time share operand rows in both directions.
+__device__ __forceinline__ void mx_tile(uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+    const uint32_t total = tiles_m * tiles_n, q = total >> 3, rem = total & 7;
+    const uint32_t x = blockIdx.x & 7, local = blockIdx.x >> 3;
+    const uint32_t t = x * q + (x < rem ? x : rem) + local;
+    const uint32_t band = t / (4 * tiles_n), first = 4 * band;
+    const uint32_t h = tiles_m - first < 4 ? tiles_m - first : 4;
+    const uint32_t w = t - first * tiles_n;
+    tm = first + w % h;
+    tn = w / h;
+}
+
+// ------------------------------------------------------- few rows of X ----
+// Streaming the weight once is the bound.  No LDS staging; a
+// workgroup of NW wavefronts owns 16 RT weight rows and its wavefronts take
+// the super-steps of 128 k in turn (wave w: w, w + NW, ...), NPW of them per
+// round with all loads issued first.  Partial sums meet in LDS in wave order.
+// A lane holds row l % 16 and block c = l / 16 of the super-step: 16 bytes of
+// codes and one scale byte.  The bf16 form's four MFMAs of 32 k take the k of
+// a lane's block in order (lane group c, MFMA j: k = 32 c + 8 j), the same
+// for both operands.
+template <bool A4, bool BF16, int MB, int RT, int NW, int NPW>
+__global__ void __launch_bounds__(64 * NW) mx_gemm_skinny_kernel(MxGemmArgs a) {
+    __shared__ float red[NW][MB][RT][16][17];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r16 = lane & 15, c = lane >> 4;
+    const int64_t tiles_n = (a.N + 16 * RT - 1) / (16 * RT), tile_m = blockIdx.x / tiles_n;
+    const int64_t n0 = (blockIdx.x - tile_m * tiles_n) * 16 * RT, m0 = tile_m * 16 * MB;
+    const int nb = (int)(a.K >> 5);            // blocks of a row
+    const int nss = (nb + 3) >> 2;             // super-steps
+    const uint8_t *wrow[RT], *wsc[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        int64_t n = n0 + rt * 16 + r16;
+        if (n >= a.N) n = a.N - 1;
+        wrow[rt] = a.wp + n * (a.K >> 1);
+        wsc[rt] = a.ws + n * nb;
+    }
+    const uint8_t *xrow[MB], *xsc[MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        int64_t m = m0 + mb * 16 + r16;
+        if (m >= a.M) m = a.M - 1;
+        if constexpr (A4) {
+            xrow[mb] = a.xp + m * (a.K >> 1);
+            xsc[mb] = a.xs + m * nb;
+        } else {
+            xrow[mb] = reinterpret_cast<const uint8_t*>(a.x + m * a.K);
         }
     }
-    if (n0 + r >= a.N) return;
+    f32x4 acc[MB][RT];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t mm = m0 + (i >> 2) * 8 + half * 4 + (i & 3);
-        if (mm < a.M) store_acc<BF16>(a.y, mm * a.N + n0 + r, acc[i]);
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[mb][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    constexpr int XJ = A4 ? 1 : 4;
+    for (int base = wave; base < nss; base += NW * NPW) {
+        u32x4 w[NPW][RT], x[NPW][MB][XJ];
+        uint32_t ws[NPW][RT], xs[NPW][MB];
+#pragma unroll
+        for (int i = 0; i < NPW; ++i) {
+            const int b = (base + NW * i) * 4 + c;   // this lane's block
+            const bool in = b < nb;
+            const int64_t bb = in ? b : 0;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                w[i][rt] = *reinterpret_cast<const u32x4*>(wrow[rt] + bb * 16);
+                ws[i][rt] = wsc[rt][bb];
+            }
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                if constexpr (A4) {
+                    x[i][mb][0] = *reinterpret_cast<const u32x4*>(xrow[mb] + bb * 16);
+                    xs[i][mb] = xsc[mb][bb];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[i][mb][j] = *reinterpret_cast<const u32x4*>(xrow[mb] + bb * 64 + 16 * j);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NPW; ++i) {
+            const int ss = base + NW * i;
+            if (ss >= nss) break;
+            if (ss * 4 + 4 > nb) {   // the last super-step of a K that is no multiple of 128
+                const bool in = ss * 4 + c < nb;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    w[i][rt] = in ? w[i][rt] : u32x4{0u, 0u, 0u, 0u};
+                    ws[i][rt] = in ? ws[i][rt] : 0u;
+                }
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+#pragma unroll
+                    for (int j = 0; j < XJ; ++j) x[i][mb][j] = in ? x[i][mb][j] : u32x4{0u, 0u, 0u, 0u};
+                    if constexpr (A4) xs[i][mb] = in ? xs[i][mb] : 0u;
+                }
+            }
+            if constexpr (A4) {
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        acc[mb][rt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            fp4_operand(x[i][mb][0]), fp4_operand(w[i][rt]), acc[mb][rt], 4, 4, 0, (int)xs[i][mb], 0,
+                            (int)ws[i][rt]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const bf16x8 wf = unpack8(w[i][rt][j], scale_f32(ws[i][rt]));
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb)
+                            acc[mb][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8, x[i][mb][j]), wf, acc[mb][rt], 0, 0, 0);
+                    }
+            }
+        }
+    }
+    // C of a 16 x 16 MFMA: lane l, element r -> row 4 (l / 16) + r, column l % 16
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[wave][mb][rt][4 * c + r][r16] = acc[mb][rt][r];
+    __syncthreads();
+    for (int t = threadIdx.x; t < MB * 256 * RT; t += 64 * NW) {
+        const int j = t % 16, rt = (t / 16) % RT, i = (t / (16 * RT)) % 16, mb = t / (256 * RT);
+        const int64_t m = m0 + mb * 16 + i, n = n0 + rt * 16 + j;
+        if (m >= a.M || n >= a.N) continue;
+        float sum = red[0][mb][rt][i][j];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) sum += red[w][mb][rt][i][j];
+        store_y<BF16>(a.y, m * a.N + n, sum);
     }
 }
 
-template <bool A4>
-hipError_t launch_direct(const MxGemmArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(((a.N + 127) / 128) * ((a.M + 31) / 32)));
-    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_direct_kernel<A4, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((mx_gemm_direct_kernel<A4, false>), grid, dim3(256), 0, stream, a);
-    return hipGetLastError();
+// ------------------------------------------------------ many rows of X ----
+// BM x BN outputs per workgroup, NWM x NWN wavefronts in 32 x 32 MFMA blocks.
+// A stage holds KS bytes of each operand row in LDS, moved there by
+// global_load_lds_dwordx4 (64 lanes x 16 bytes per instruction), two stages:
+// stage kt + 1 is in flight while kt computes, one barrier per stage.  A row
+// of KS bytes has KS / 16 slots and 256 / KS rows fill the 64 banks: piece p
+// of row r lies in slot p ^ ((r / rows) % slots), so the 16 rows that a
+// fragment read serves at a time hit distinct banks.
+template <int KS>
+__device__ __forceinline__ int lds_at(int row, int piece) {
+    constexpr int SLOTS = KS / 16, ROWS = 256 / KS;
+    return row * KS + ((piece ^ ((row / ROWS) % SLOTS)) << 4);
+}
+
+// Moves a wavefront's share of ROWS rows of KS bytes per stage with buffer
+// loads into LDS: a scalar stage offset, fixed 32-bit lane offsets, and zeros
+// for what lies past the matrix (rows past its end, and the last row's
+// pieces past K; other rows' pieces past K are the next row's, which the
+// caller masks).
+template <int ROWS, int KS, int NW>
+struct Mover {
+    static constexpr int SLOTS = KS / 16, RPI = 64 / SLOTS;   // rows per instruction
+    static constexpr int Q = ROWS / RPI / NW;                 // instructions per wavefront and stage
+    static_assert(Q * RPI * NW == ROWS, "rows must split evenly over the wavefronts");
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t off[Q];
+    int wave;
+    __device__ __forceinline__ void init(const void* base, int64_t row0, int64_t rows, int64_t pitch, int w) {
+        const int lane = threadIdx.x & 63;
+        wave = w;
+        // the offsets stay below 256 pitch + KS < 2^32, so a longer remainder may be cut there
+        const int64_t left = (rows - row0) * pitch;
+        const uint32_t num = left < 0xFFFFFFFFll ? (uint32_t)left : 0xFFFFFFFFu;
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(static_cast<const uint8_t*>(base) + row0 * pitch), 0, (int)num, 0x00020000);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int r = (q * NW + w) * RPI + lane / SLOTS;
+            const int piece = (lane % SLOTS) ^ ((r / (256 / KS)) % SLOTS);
+            off[q] = (uint32_t)r * (uint32_t)pitch + (uint32_t)piece * 16u;
+        }
+    }
+    __device__ __forceinline__ void issue(char* lds, int kt) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (q * NW + wave) * 1024), 16, (int)off[q],
+                                                     kt * KS, 0, 0);
+    }
+};
+
+// Row r's offset into a matrix of pitch `pitch`, relative to row0, clamped to
+// the last row.
+__device__ __forceinline__ uint32_t row_offset(int64_t row0, int r, int64_t rows, int64_t pitch) {
+    const int64_t last = rows - 1 - row0;
+    return (uint32_t)((r < last ? r : last) * pitch);
+}
+
+// Writes a wavefront's blocks of the tile at (m0, n0): element e of a block is
+// row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.  Buffer stores with
+// 32-bit offsets (kMxTileMaxN) from the tile's first row drop rows past M.
+template <int TM, int TN, bool BF16>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[TM][TN], const MxGemmArgs& a, int64_t m0, int64_t n0,
+                                           int wr, int wc) {
+    constexpr uint32_t ES = BF16 ? 2 : 4;
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int64_t left = (a.M - m0) * a.N * ES;
+    const uint32_t pitch = (uint32_t)a.N * ES;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t*>(a.y) + m0 * a.N * ES, 0,
+                                                        left < 0xFFFFFFFFll ? (int)left : -1, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        const int64_t n = n0 + wc + j * 32 + (lane & 31);
+        if (n >= a.N) continue;
+        const uint32_t at = (uint32_t)(wr + 4 * half) * pitch + (uint32_t)n * ES;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t o = at + (uint32_t)(i * 32 + (e >> 2) * 8 + (e & 3)) * pitch;
+                const float v = acc[i][j][e];
+                if constexpr (BF16)
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16x2(v, v), rsrc, (int)o, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rsrc, (int)o, 0, 0);
+            }
+    }
+}
+
+// Both operands packed, K >= 256: a stage is 256 k (128 bytes a row), four
+// MFMA steps of 64 k.  A lane holds row l % 32 and blocks 2 s + l / 32, s =
+// 0..3, of the stage: its eight scale bytes come as two dwords straight from
+// global memory one stage ahead, and one byte permute leaves its four in the
+// order of the steps, where the MFMA's operand selects take them.  Blocks past
+// K get scale byte 0 on both sides: their products, at most 36 * 2^-254, are
+// zeros in fp32.
+template <int BM, int BN, int NWM, int NWN, bool BF16>
+__global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmArgs a) {
+    constexpr int NW = NWM * NWN, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32, KS = 128;
+    __shared__ __attribute__((aligned(1024))) char sx0[BM * KS], sw0[BN * KS], sx1[BM * KS], sw1[BN * KS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / NWN, wn = wave % NWN, r = lane & 31, half = lane >> 5;
+    uint32_t tile_m, tile_n;
+    mx_tile((uint32_t)((a.M + BM - 1) / BM), (uint32_t)((a.N + BN - 1) / BN), tile_m, tile_n);
+    const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
+    const int nb = (int)(a.K >> 5), nk = (nb + 7) >> 3;
+
+    Mover<BM, KS, NW> mx;
+    Mover<BN, KS, NW> mw;
+    mx.init(a.xp, m0, a.M, a.K >> 1, wave);
+    mw.init(a.wp, n0, a.N, a.K >> 1, wave);
+    const uint8_t *xs = a.xs + m0 * nb, *ws = a.ws + n0 * nb;
+    uint32_t xo[TM], wo[TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xo[i] = row_offset(m0, wm * WM + i * 32 + r, a.M, nb);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wo[i] = row_offset(n0, wn * WN + i * 32 + r, a.N, nb);
+    const uint32_t sel = half ? 0x07050301u : 0x06040200u;
+    // The scale bytes of stage kt as they lie in memory: eight from block 8 kt,
+    // or in the last, partial stage the row's last eight, which use() shifts
+    // down (zeros follow).
+    uint64_t nx[TM], nw[TN];
+    auto load_scales = [&](int kt) __attribute__((always_inline)) {
+        const int b = kt * 8 < nb - 8 ? kt * 8 : nb - 8;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) __builtin_memcpy(&nx[i], xs + b + xo[i], 8);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) __builtin_memcpy(&nw[i], ws + b + wo[i], 8);
+    };
+    auto use = [&](uint64_t v, int kt) __attribute__((always_inline)) {
+        const int past = kt * 8 - (nb - 8);
+        v >>= past > 0 ? 8 * past : 0;
+        return __builtin_amdgcn_perm((uint32_t)(v >> 32), (uint32_t)v, sel);
+    };
+
+    f32x16 acc[TM][TN] = {};
+    mx.issue(sx0, 0);
+    mw.issue(sw0, 0);
+    load_scales(0);
+
+    auto stage = [&](int kt, auto par) __attribute__((always_inline)) {
+        constexpr int P = decltype(par)::value;
+        const char* X = P ? sx1 : sx0;
+        const char* W = P ? sw1 : sw0;
+        wait_vmcnt<0>();
+        lds_barrier();   // stage kt has landed everywhere; everyone is done with stage kt - 1
+        uint32_t cx[TM], cw[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) cx[i] = use(nx[i], kt);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) cw[i] = use(nw[i], kt);
+        // fragments of step s + 1 are read while step s multiplies
+        u32x4 xf[2][TM], wf[2][TN];
+        auto frags = [&](auto S) __attribute__((always_inline)) {
+            constexpr int s = decltype(S)::value;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                xf[s & 1][i] = *reinterpret_cast<const u32x4*>(X + lds_at<KS>(wm * WM + i * 32 + r, 2 * s + half));
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                wf[s & 1][i] = *reinterpret_cast<const u32x4*>(W + lds_at<KS>(wn * WN + i * 32 + r, 2 * s + half));
+        };
+        frags(std::integral_constant<int, 0>{});
+        // the stage past the last repeats it: read by no one
+        const int next = kt + 1 < nk ? kt + 1 : kt;
+        mx.issue(P ? sx0 : sx1, next);
+        mw.issue(P ? sw0 : sw1, next);
+        load_scales(next);
+        gemm::static_for<4>([&](auto S) {
+            constexpr int s = decltype(S)::value;
+            if constexpr (s < 3) frags(std::integral_constant<int, s + 1>{});
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        fp4_operand(xf[s & 1][i]), fp4_operand(wf[s & 1][j]), acc[i][j], 4, 4, s, (int)cx[i], s,
+                        (int)cw[j]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    int kt = 0;
+    for (; kt + 2 <= nk; kt += 2) {
+        stage(kt, std::integral_constant<int, 0>{});
+        stage(kt + 1, std::integral_constant<int, 1>{});
+    }
+    if (kt < nk) stage(kt, std::integral_constant<int, 0>{});
+    wait_vmcnt<0>();   // the last, unread loads into LDS
+
+    store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
+}
+
+// bf16 activations: a stage is 64 k, 128 bytes of an X row and 32 of a W row.
+// A lane's 16 bytes of codes are one block (half l / 32 of the stage), which
+// the stage's four MFMAs of 16 k take in order (lane half h, MFMA j: k = 32 h
+// + 8 j, the same for X); it is unpacked in registers with the lane's one
+// scale byte, fetched a stage ahead.  Where K ends in half a stage, the upper
+// lanes multiply zeros there.
+template <int BM, int BN, int NWM, int NWN, bool BF16>
+__global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a16_tile_kernel(MxGemmArgs a) {
+    constexpr int NW = NWM * NWN, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32;
+    __shared__ __attribute__((aligned(1024))) char sx0[BM * 128], sw0[BN * 32], sx1[BM * 128], sw1[BN * 32];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / NWN, wn = wave % NWN, r = lane & 31, half = lane >> 5;
+    uint32_t tile_m, tile_n;
+    mx_tile((uint32_t)((a.M + BM - 1) / BM), (uint32_t)((a.N + BN - 1) / BN), tile_m, tile_n);
+    const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
+    const int nb = (int)(a.K >> 5), nk = (nb + 1) >> 1;
+
+    Mover<BM, 128, NW> mx;
+    Mover<BN, 32, NW> mw;
+    mx.init(a.x, m0, a.M, 2 * a.K, wave);
+    mw.init(a.wp, n0, a.N, a.K >> 1, wave);
+    const uint8_t* ws = a.ws + n0 * nb;
+    uint32_t wo[TN], nw[TN];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wo[i] = row_offset(n0, wn * WN + i * 32 + r, a.N, nb);
+    auto load_scales = [&](int kt) __attribute__((always_inline)) {
+        const int b = 2 * kt + half;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) nw[i] = ws[wo[i] + (uint32_t)(b < nb ? b : nb - 1)];
+    };
+    f32x16 acc[TM][TN] = {};
+    mx.issue(sx0, 0);
+    mw.issue(sw0, 0);
+    load_scales(0);
+
+    // CUT: only the lower half of the stage is within K
+    auto stage = [&](int kt, const char* X, const char* W, char* nextX, char* nextW, auto cut)
+                     __attribute__((always_inline)) {
+        constexpr bool CUT = decltype(cut)::value;
+        const uint32_t keep = CUT && half ? 0u : ~0u;
+        wait_vmcnt<0>();
+        lds_barrier();
+        float sc[TN];
+#pragma unroll
+        for (int i = 0; i < TN; ++i) sc[i] = scale_f32(nw[i]);
+        u32x4 codes[TN], xf[2][TM];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            codes[j] = *reinterpret_cast<const u32x4*>(W + lds_at<32>(wn * WN + j * 32 + r, half));
+            if constexpr (CUT) codes[j] &= keep;
+        }
+        auto frags = [&](auto S) __attribute__((always_inline)) {
+            constexpr int s = decltype(S)::value;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                xf[s & 1][i] = *reinterpret_cast<const u32x4*>(X + lds_at<128>(wm * WM + i * 32 + r, 4 * half + s));
+                if constexpr (CUT) xf[s & 1][i] &= keep;
+            }
+        };
+        frags(std::integral_constant<int, 0>{});
+        if constexpr (!CUT) {
+            const int next = kt + 1 < nk ? kt + 1 : kt;   // the stage past the last repeats it: read by no one
+            mx.issue(nextX, next);
+            mw.issue(nextW, next);
+            load_scales(next);
+        }
+        gemm::static_for<4>([&](auto S) {
+            constexpr int s = decltype(S)::value;
+            if constexpr (s < 3) frags(std::integral_constant<int, s + 1>{});
+            bf16x8 wf[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) wf[j] = unpack8(codes[j][s], sc[j]);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, xf[s & 1][i]), wf[j],
+                                                                        acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    const int whole = nb >> 1;
+    int kt = 0;
+    for (; kt + 2 <= whole; kt += 2) {
+        stage(kt, sx0, sw0, sx1, sw1, std::false_type{});
+        stage(kt + 1, sx1, sw1, sx0, sw0, std::false_type{});
+    }
+    if (kt < whole) stage(kt, sx0, sw0, sx1, sw1, std::false_type{});
+    if (nb & 1) stage(whole, whole & 1 ? sx1 : sx0, whole & 1 ? sw1 : sw0, nullptr, nullptr, std::true_type{});
+    wait_vmcnt<0>();   // the last, unread loads into LDS
+
+    store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
+}
+
+template <bool A4, int MB, int RT, int NW, int NPW>
+void launch_skinny(const MxGemmArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(((a.N + 16 * RT - 1) / (16 * RT)) * ((a.M + 16 * MB - 1) / (16 * MB)))), block(64 * NW);
+    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_skinny_kernel<A4, true, MB, RT, NW, NPW>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((mx_gemm_skinny_kernel<A4, false, MB, RT, NW, NPW>), grid, block, 0, stream, a);
+}
+
+template <int BM, int BN>
+dim3 tile_grid(const MxGemmArgs& a) {
+    return dim3((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN)));
+}
+template <int BM, int BN, int NWM, int NWN>
+void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
+    const dim3 block(NWM * NWN * 64);
+    if (a.y_bf16)
+        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, true>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, false>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
+}
+template <int BM, int BN, int NWM, int NWN>
+void launch_a16_tile(const MxGemmArgs& a, hipStream_t stream) {
+    const dim3 block(NWM * NWN * 64);
+    if (a.y_bf16)
+        hipLaunchKernelGGL((mx_gemm_a16_tile_kernel<BM, BN, NWM, NWN, true>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((mx_gemm_a16_tile_kernel<BM, BN, NWM, NWN, false>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
 }
 
 }  // namespace
 
-hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) { return launch_direct<false>(a, stream); }
-hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) { return launch_direct<true>(a, stream); }
+hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
+    if (a.M <= 16) launch_skinny<false, 1, 1, 16, 2>(a, stream);
+    else if (a.M <= 32) launch_skinny<false, 2, 1, 16, 1>(a, stream);
+    else if (a.M <= 64 || a.N >= kMxTileMaxN) launch_skinny<false, 4, 1, 8, 1>(a, stream);
+    else launch_a16_tile<256, 256, 2, 4>(a, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
+    if (a.M <= 16) launch_skinny<true, 1, 1, 16, 2>(a, stream);
+    else if (a.M <= 32) launch_skinny<true, 2, 1, 16, 2>(a, stream);
+    else if (a.M <= 64 || a.K < 256 || a.N >= kMxTileMaxN) launch_skinny<true, 4, 1, 16, 1>(a, stream);
+    else launch_a4_tile<256, 256, 2, 4>(a, stream);
+    return hipGetLastError();
+}
 
 }  // namespace ar
