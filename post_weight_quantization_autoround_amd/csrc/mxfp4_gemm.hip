@@ -6,6 +6,7 @@
 //
 // K is a multiple of 32, so a 16-byte piece of packed codes is one block.
 #include <type_traits>
+#include <cstdlib>
 
 #include "ar_internal.h"
 #include "gemm_tiles.h"
@@ -236,9 +237,10 @@ struct Mover {
             off[q] = (uint32_t)r * (uint32_t)pitch + (uint32_t)piece * 16u;
         }
     }
-    __device__ __forceinline__ void issue(char* lds, int kt) {
+    // instructions [part Q / parts, (part + 1) Q / parts) of stage kt
+    __device__ __forceinline__ void issue(char* lds, int kt, int part = 0, int parts = 1) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
+        for (int q = part * Q / parts; q < (part + 1) * Q / parts; ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (q * NW + wave) * 1024), 16, (int)off[q],
                                                      kt * KS, 0, 0);
     }
@@ -282,17 +284,62 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[TM][TN], const Mx
     }
 }
 
+// Scale bytes of the packed-activation tiles.  A row's scales of a stage are
+// eight bytes and rows lie K / 32 bytes apart, so fetching a stage at a time
+// takes a cache line per row and stage (100 of 575 us at 4096 x 28672 x 8192).
+// Where rows are dword-aligned (K a multiple of 128) they come in groups of
+// four stages instead, 32 bytes a row, moved to LDS a quarter of the rows per
+// stage: two groups of (BM + BN) * 32 bytes.  Row r's eight-byte piece p lies
+// at p ^ (r / 8 % 4), which spreads the 32 rows that a read takes over all
+// banks.
+template <int BM, int BN, int NW>
+struct ScaleMover {
+    static constexpr int ROWS = BM + BN, QR = ROWS / 4, T = QR / (8 * NW);   // 8 rows per instruction
+    static_assert(BM == BN && T * 8 * NW == QR, "quarters must be of one operand and split over the wavefronts");
+    __amdgpu_buffer_rsrc_t rx, rw;
+    uint32_t off[T];
+    uint32_t nb;
+    int wave;
+    __device__ __forceinline__ void init(const uint8_t* xs, int64_t xrows, const uint8_t* ws, int64_t wrows, int n, int w) {
+        const int lane = threadIdx.x & 63;
+        wave = w;
+        nb = (uint32_t)n;
+        auto rsrc = [&](const uint8_t* p, int64_t rows) {
+            const int64_t left = rows * n;   // offsets stay below (256 + 1) nb < 2^27
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0,
+                                                     left < 0x7FFFFFFFll ? (int)left : 0x7FFFFFFF, 0x00020000);
+        };
+        rx = rsrc(xs, xrows);
+        rw = rsrc(ws, wrows);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            const int r = (t * NW + w) * 8 + lane / 8;   // a row of the quarter; r / 8 % 4 as in the whole
+            off[t] = (uint32_t)r * nb + (uint32_t)(((((lane % 8) >> 1) ^ ((r / 8) & 3)) << 3) + (lane & 1) * 4);
+        }
+    }
+    // quarter q of group g
+    __device__ __forceinline__ void issue(char* lds, int g, int q) {
+        const uint32_t o = (uint32_t)(q & 1) * QR * nb + (uint32_t)g * 32u;
+        char* at = lds + (g & 1) * ROWS * 32 + q * QR * 32;
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? rx : rw, (lds_void*)(at + (t * NW + wave) * 256), 4,
+                                                     (int)(off[t] + o), 0, 0, 0);
+    }
+};
+
 // Both operands packed, K >= 256: a stage is 256 k (128 bytes a row), four
 // MFMA steps of 64 k.  A lane holds row l % 32 and blocks 2 s + l / 32, s =
-// 0..3, of the stage: its eight scale bytes come as two dwords straight from
-// global memory one stage ahead, and one byte permute leaves its four in the
-// order of the steps, where the MFMA's operand selects take them.  Blocks past
-// K get scale byte 0 on both sides: their products, at most 36 * 2^-254, are
-// zeros in fp32.
-template <int BM, int BN, int NWM, int NWN, bool BF16>
+// 0..3, of the stage: one byte permute of the row's eight scale bytes leaves
+// its four in the order of the steps, where the MFMA's operand selects take
+// them.  GROUPED: scales by ScaleMover; otherwise straight from global memory
+// a stage ahead.  Blocks past K get scale byte 0 on both sides: their
+// products, at most 36 * 2^-254, are zeros in fp32.
+template <int BM, int BN, int NWM, int NWN, bool BF16, bool GROUPED>
 __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmArgs a) {
     constexpr int NW = NWM * NWN, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32, KS = 128;
     __shared__ __attribute__((aligned(1024))) char sx0[BM * KS], sw0[BN * KS], sx1[BM * KS], sw1[BN * KS];
+    __shared__ __attribute__((aligned(1024))) char ssc[GROUPED ? 2 * (BM + BN) * 32 : 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / NWN, wn = wave % NWN, r = lane & 31, half = lane >> 5;
     uint32_t tile_m, tile_n;
@@ -305,81 +352,127 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmA
     mx.init(a.xp, m0, a.M, a.K >> 1, wave);
     mw.init(a.wp, n0, a.N, a.K >> 1, wave);
     const uint8_t *xs = a.xs + m0 * nb, *ws = a.ws + n0 * nb;
-    uint32_t xo[TM], wo[TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) xo[i] = row_offset(m0, wm * WM + i * 32 + r, a.M, nb);
-#pragma unroll
-    for (int i = 0; i < TN; ++i) wo[i] = row_offset(n0, wn * WN + i * 32 + r, a.N, nb);
     const uint32_t sel = half ? 0x07050301u : 0x06040200u;
-    // The scale bytes of stage kt as they lie in memory: eight from block 8 kt,
-    // or in the last, partial stage the row's last eight, which use() shifts
-    // down (zeros follow).
     uint64_t nx[TM], nw[TN];
+    uint32_t xo[TM], wo[TN];
+    ScaleMover<BM, BN, NW> ms;
+    if constexpr (GROUPED) {
+        ms.init(xs, a.M - m0, ws, a.N - n0, nb, wave);
+    } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) xo[i] = row_offset(m0, wm * WM + i * 32 + r, a.M, nb);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) wo[i] = row_offset(n0, wn * WN + i * 32 + r, a.N, nb);
+    }
+    // The scale bytes of stage kt.  Not GROUPED, the last, partial stage reads
+    // the row's last eight.
     auto load_scales = [&](int kt) __attribute__((always_inline)) {
-        const int b = kt * 8 < nb - 8 ? kt * 8 : nb - 8;
+        if constexpr (GROUPED) {
+            const char* g = ssc + ((kt >> 2) & 1) * (BM + BN) * 32 + r * 32 + (((kt & 3) ^ ((r >> 3) & 3)) << 3);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) __builtin_memcpy(&nx[i], xs + b + xo[i], 8);
+            for (int i = 0; i < TM; ++i) nx[i] = *reinterpret_cast<const uint64_t*>(g + (wm * WM + i * 32) * 32);
 #pragma unroll
-        for (int i = 0; i < TN; ++i) __builtin_memcpy(&nw[i], ws + b + wo[i], 8);
+            for (int i = 0; i < TN; ++i) nw[i] = *reinterpret_cast<const uint64_t*>(g + (BM + wn * WN + i * 32) * 32);
+        } else {
+            const int b = kt * 8 < nb - 8 ? kt * 8 : nb - 8;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) __builtin_memcpy(&nx[i], xs + b + xo[i], 8);
+#pragma unroll
+            for (int i = 0; i < TN; ++i) __builtin_memcpy(&nw[i], ws + b + wo[i], 8);
+        }
     };
     auto use = [&](uint64_t v, int kt) __attribute__((always_inline)) {
-        const int past = kt * 8 - (nb - 8);
-        v >>= past > 0 ? 8 * past : 0;
+        const int past = kt * 8 - (nb - 8);   // blocks of the stage past K
+        if constexpr (GROUPED) v &= ~0ull >> (past > 0 ? 8 * (past < 8 ? past : 7) : 0);
+        else v >>= past > 0 ? 8 * (past < 8 ? past : 7) : 0;
         return __builtin_amdgcn_perm((uint32_t)(v >> 32), (uint32_t)v, sel);
     };
 
     f32x16 acc[TM][TN] = {};
-    mx.issue(sx0, 0);
-    mw.issue(sw0, 0);
-    load_scales(0);
-
-    auto stage = [&](int kt, auto par) __attribute__((always_inline)) {
-        constexpr int P = decltype(par)::value;
-        const char* X = P ? sx1 : sx0;
-        const char* W = P ? sw1 : sw0;
-        wait_vmcnt<0>();
-        lds_barrier();   // stage kt has landed everywhere; everyone is done with stage kt - 1
-        uint32_t cx[TM], cw[TN];
+    uint32_t cx[TM], cw[TN];
+    auto use_scales = [&](int kt) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < TM; ++i) cx[i] = use(nx[i], kt);
 #pragma unroll
         for (int i = 0; i < TN; ++i) cw[i] = use(nw[i], kt);
-        // fragments of step s + 1 are read while step s multiplies
-        u32x4 xf[2][TM], wf[2][TN];
-        auto frags = [&](auto S) __attribute__((always_inline)) {
-            constexpr int s = decltype(S)::value;
+    };
+    u32x4 xf[2][TM], wf[2][TN];
+    // fragment f (X's, then W's) of step s from LDS into register set s % 2
+    auto frag = [&](const char* X, const char* W, auto S, auto F) __attribute__((always_inline)) {
+        constexpr int s = decltype(S)::value, f = decltype(F)::value;
+        if constexpr (f < TM)
+            xf[s & 1][f] = *reinterpret_cast<const u32x4*>(X + (wm * WM + f * 32) * KS + lds_at<KS>(r, 2 * s + half));
+        else
+            wf[s & 1][f - TM] = *reinterpret_cast<const u32x4*>(W + (wn * WN + (f - TM) * 32) * KS + lds_at<KS>(r, 2 * s + half));
+    };
+    using I0 = std::integral_constant<int, 0>;
+
+    if constexpr (GROUPED)
+        for (int q = 0; q < 4; ++q) ms.issue(ssc, 0, q);
+    mx.issue(sx0, 0);
+    mw.issue(sw0, 0);
+    if constexpr (!GROUPED) load_scales(0);
+    wait_vmcnt<0>();
+    lds_barrier();
+    if constexpr (GROUPED) load_scales(0);
+    use_scales(0);
+    mx.issue(sx1, nk > 1 ? 1 : 0);
+    mw.issue(sw1, nk > 1 ? 1 : 0);
+    if constexpr (GROUPED) ms.issue(ssc, 1, 0);
+    else load_scales(nk > 1 ? 1 : 0);
+    gemm::static_for<TM + TN>([&](auto F) { frag(sx0, sw0, I0{}, F); });
+
+    // Stage kt, its data in X, W: during step s the fragments of step s + 1 are
+    // read.  Before the last step the next stage has landed and every wave
+    // holds its last fragments of this one, so one barrier there frees X, W for
+    // stage kt + 2 and the next stage's first fragments are read in that step.
+    // The scales of stage kt + 1 are read there too, so from the barrier of
+    // stage 4 g - 1 on group g - 1 is done with and group g + 1 takes its place.
+    // (Past the last stage the loads repeat it and the fragments are unused.)
+    auto stage = [&](int kt, char* X, char* W, const char* X1, const char* W1) __attribute__((always_inline)) {
+        uint32_t ex[TM], ew[TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-                xf[s & 1][i] = *reinterpret_cast<const u32x4*>(X + lds_at<KS>(wm * WM + i * 32 + r, 2 * s + half));
+        for (int i = 0; i < TM; ++i) ex[i] = cx[i];
 #pragma unroll
-            for (int i = 0; i < TN; ++i)
-                wf[s & 1][i] = *reinterpret_cast<const u32x4*>(W + lds_at<KS>(wn * WN + i * 32 + r, 2 * s + half));
-        };
-        frags(std::integral_constant<int, 0>{});
-        // the stage past the last repeats it: read by no one
-        const int next = kt + 1 < nk ? kt + 1 : kt;
-        mx.issue(P ? sx0 : sx1, next);
-        mw.issue(P ? sw0 : sw1, next);
-        load_scales(next);
+        for (int i = 0; i < TN; ++i) ew[i] = cw[i];
+        const int next = kt + 2 < nk ? kt + 2 : nk - 1;
         gemm::static_for<4>([&](auto S) {
-            constexpr int s = decltype(S)::value;
-            if constexpr (s < 3) frags(std::integral_constant<int, s + 1>{});
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                        fp4_operand(xf[s & 1][i]), fp4_operand(wf[s & 1][j]), acc[i][j], 4, 4, s, (int)cx[i], s,
-                        (int)cw[j]);
-            __builtin_amdgcn_sched_barrier(0);
+            constexpr int s = decltype(S)::value, n = TM * TN;
+            if constexpr (s == 3) {
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                if constexpr (GROUPED) {
+                    load_scales(kt + 1);
+                    use_scales(kt + 1);
+                    ms.issue(ssc, ((kt + 1) >> 2) + 1, (kt + 1) & 3);
+                } else {
+                    use_scales(kt + 1);
+                    load_scales(next);
+                }
+            }
+            gemm::static_for<n>([&](auto Kk) {
+                constexpr int k = decltype(Kk)::value, i = k / TN, j = k % TN;
+                constexpr int f0 = k * (TM + TN) / n, f1 = (k + 1) * (TM + TN) / n;
+                gemm::static_for<f1 - f0>([&](auto D) {
+                    using F = std::integral_constant<int, f0 + decltype(D)::value>;
+                    if constexpr (s < 3) frag(X, W, std::integral_constant<int, s + 1>{}, F{});
+                    else frag(X1, W1, I0{}, F{});
+                });
+                if constexpr (s == 3) {
+                    mx.issue(X, next, k, n);
+                    mw.issue(W, next, k, n);
+                }
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fp4_operand(xf[s & 1][i]), fp4_operand(wf[s & 1][j]), acc[i][j], 4, 4, s, (int)ex[i], s, (int)ew[j]);
+                __builtin_amdgcn_sched_barrier(0);
+            });
         });
     };
     int kt = 0;
     for (; kt + 2 <= nk; kt += 2) {
-        stage(kt, std::integral_constant<int, 0>{});
-        stage(kt + 1, std::integral_constant<int, 1>{});
+        stage(kt, sx0, sw0, sx1, sw1);
+        stage(kt + 1, sx1, sw1, sx0, sw0);
     }
-    if (kt < nk) stage(kt, std::integral_constant<int, 0>{});
+    if (kt < nk) stage(kt, sx0, sw0, sx1, sw1);
     wait_vmcnt<0>();   // the last, unread loads into LDS
 
     store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
@@ -490,13 +583,19 @@ template <int BM, int BN>
 dim3 tile_grid(const MxGemmArgs& a) {
     return dim3((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN)));
 }
+template <int BM, int BN, int NWM, int NWN, bool BF16>
+void launch_a4_tile_y(const MxGemmArgs& a, hipStream_t stream) {
+    const dim3 grid = tile_grid<BM, BN>(a), block(NWM * NWN * 64);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
+    if (a.K % 128 == 0 && aligned)
+        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, BF16, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, BF16, false>), grid, block, 0, stream, a);
+}
 template <int BM, int BN, int NWM, int NWN>
 void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
-    const dim3 block(NWM * NWN * 64);
-    if (a.y_bf16)
-        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, true>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, false>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
+    if (a.y_bf16) launch_a4_tile_y<BM, BN, NWM, NWN, true>(a, stream);
+    else launch_a4_tile_y<BM, BN, NWM, NWN, false>(a, stream);
 }
 template <int BM, int BN, int NWM, int NWN>
 void launch_a16_tile(const MxGemmArgs& a, hipStream_t stream) {
@@ -521,6 +620,7 @@ hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
     if (a.M <= 16) launch_skinny<true, 1, 1, 16, 2>(a, stream);
     else if (a.M <= 32) launch_skinny<true, 2, 1, 16, 2>(a, stream);
     else if (a.M <= 64 || a.K < 256 || a.N >= kMxTileMaxN) launch_skinny<true, 4, 1, 16, 1>(a, stream);
+    else if (getenv("MXC") && atoi(getenv("MXC"))==1) launch_a4_tile<256, 256, 2, 2>(a, stream);
     else launch_a4_tile<256, 256, 2, 4>(a, stream);
     return hipGetLastError();
 }
