@@ -572,6 +572,283 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a16_tile_kernel(MxGemm
     store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
 }
 
+// --------------------------------------------------- a few hundred rows ----
+// Tiles too small for a wavefront to own a full K: NWM x NWN wavefronts cover
+// BM x BN outputs and NWK such sets split every stage between them; their sums
+// meet in LDS at the end, in order.  A ring of four stages in LDS keeps three
+// in flight.  A stage is SB blocks: 256 k of packed operands, or 128 k where X
+// is bf16 (256 bytes of a row, as two 128-byte rows in LDS, one per 64 k).
+// The stage's 64-k steps go to the NWK sets in runs.  In the last stage lanes
+// past K load from past the buffers, which gives zeros.
+template <int ROWS, int RB, int SUB, int NW>
+struct RingMover {
+    // LDS row s * ROWS + r holds bytes [RB s, RB s + RB) of row r's stage
+    static constexpr int SLOTS = RB / 16, RPI = 64 / SLOTS, Q = ROWS * SUB / RPI / NW;
+    static_assert(Q * RPI * NW == ROWS * SUB, "rows must split evenly over the wavefronts");
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t off[Q];
+    uint32_t col[Q];   // byte of the row's stage
+    int wave;
+    __device__ __forceinline__ void init(const void* base, int64_t row0, int64_t rows, int64_t pitch, int w) {
+        const int lane = threadIdx.x & 63;
+        wave = w;
+        const int64_t left = (rows - row0) * pitch;
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(static_cast<const uint8_t*>(base) + row0 * pitch), 0,
+            left < 0xFFFFFFF0ll ? (int)left : (int)0xFFFFFFF0, 0x00020000);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int lr = (q * NW + w) * RPI + lane / SLOTS, s = lr / ROWS, r = lr % ROWS;
+            col[q] = (uint32_t)(s * RB + (((lane % SLOTS) ^ ((lr / (256 / RB)) % SLOTS)) << 4));
+            off[q] = (uint32_t)r * (uint32_t)pitch + col[q];
+        }
+    }
+    // stage kt, `left` bytes of the row remaining
+    __device__ __forceinline__ void issue(char* lds, int kt, int left) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint32_t o = (int)col[q] < left ? off[q] + (uint32_t)(kt * RB * SUB) : 0xFFFFFFF0u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (q * NW + wave) * 1024), 16, (int)o, 0, 0,
+                                                     0);
+        }
+    }
+};
+
+// Scale bytes of ROWS rows in groups of four stages, 4 SB bytes a row: per-stage
+// reads straight from memory would take a cache line per row and stage and
+// cost more than the codes (64 x 64 tiles: 0.56 against 0.xx us a stage).
+// Rows start at any byte, so one dword more, from the aligned one before, is
+// moved (DW in all, RPI rows per instruction); the odd row pitch in LDS spreads
+// a read's rows over the banks.
+template <int ROWS, int SB, int NW>
+struct ScaleRing {
+    static constexpr int DW = SB + 1, RPI = 64 / DW;
+    static constexpr int S = (ROWS + RPI * NW - 1) / (RPI * NW), BYTES = S * NW * 256;   // instructions per wavefront, buffer
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t off[S];
+    int wave, shift;   // shift: the base pointer's bytes past a dword boundary
+    __device__ __forceinline__ void init(const uint8_t* base, int64_t rows, int nb, int w) {
+        const int lane = threadIdx.x & 63;
+        wave = w;
+        shift = (int)(reinterpret_cast<uintptr_t>(base) & 3);
+        const int64_t left = (rows * nb + shift + 3) & ~(int64_t)3;   // whole dwords that hold a byte of the matrix
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base - shift), 0,
+                                                 left < 0x7FFFFFFFll ? (int)left : 0x7FFFFFFF, 0x00020000);
+#pragma unroll
+        for (int t = 0; t < S; ++t) {
+            const int r = (t * NW + w) * RPI + lane / DW;
+            off[t] = lane < RPI * DW && r < ROWS
+                         ? (((uint32_t)r * (uint32_t)nb + (uint32_t)shift) & ~3u) + (uint32_t)(lane % DW) * 4u
+                         : 0x80000000u;
+        }
+    }
+    __device__ __forceinline__ void issue(char* lds, int g) {
+#pragma unroll
+        for (int t = 0; t < S; ++t)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (t * NW + wave) * 256), 4,
+                                                     (int)(off[t] + (uint32_t)(g * 4 * SB)), 0, 0, 0);
+    }
+    // where row r's bytes start in a buffer
+    __device__ __forceinline__ int at(int r, int nb) const {
+        return r / RPI * 256 + r % RPI * (4 * DW) + (((int)((uint32_t)r * (uint32_t)nb) + shift) & 3);
+    }
+};
+
+template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, bool BF16>
+__global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGemmArgs a) {
+    constexpr int NW = NWM * NWN * NWK, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32;
+    constexpr int NST = 4, SB = A4 ? 8 : 4, XSUB = A4 ? 1 : 2, STEPS = SB / 2, SPW = STEPS / NWK;
+    constexpr int WB = SB * 16, XB = XSUB * BM * 128;
+    constexpr int RED = NW * 16 * 36 * 4;   // half a block of every wavefront
+    constexpr int STAGE = XB + BN * WB > RED ? XB + BN * WB : RED;
+    using SX = ScaleRing<BM, SB, NW>;
+    using SW = ScaleRing<BN, SB, NW>;
+    __shared__ __attribute__((aligned(1024))) char st0[STAGE], st1[STAGE], st2[STAGE], st3[STAGE];
+    __shared__ __attribute__((aligned(1024))) char ssw[2 * SW::BYTES], ssx[A4 ? 2 * SX::BYTES : 16];
+    static_assert(SPW * NWK == STEPS, "the steps of a stage split over the sets");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wk = wave % NWK, wn = wave / NWK % NWN, wm = wave / (NWK * NWN), r = lane & 31, half = lane >> 5;
+    uint32_t tile_m, tile_n;
+    mx_tile((uint32_t)((a.M + BM - 1) / BM), (uint32_t)((a.N + BN - 1) / BN), tile_m, tile_n);
+    const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
+    const int nb = (int)(a.K >> 5), nk = (nb + SB - 1) / SB;
+
+    RingMover<BM, 128, XSUB, NW> mx;
+    RingMover<BN, WB, 1, NW> mw;
+    if constexpr (A4) mx.init(a.xp, m0, a.M, a.K >> 1, wave);
+    else mx.init(a.x, m0, a.M, 2 * a.K, wave);
+    mw.init(a.wp, n0, a.N, a.K >> 1, wave);
+    SX sx;
+    SW sw;
+    if constexpr (A4) sx.init(a.xs + m0 * nb, a.M - m0, nb, wave);
+    sw.init(a.ws + n0 * nb, a.N - n0, nb, wave);
+    int xo[TM], wo[TN];   // this lane's first scale byte of a group, per row block
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xo[i] = A4 ? sx.at(wm * WM + i * 32 + r, nb) + 2 * wk * SPW + half : 0;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wo[i] = sw.at(wn * WN + i * 32 + r, nb) + 2 * wk * SPW + half;
+
+    constexpr int LPW = decltype(mx)::Q + decltype(mw)::Q;   // loads per wavefront and stage
+    constexpr int SPG = SW::S + (A4 ? SX::S : 0);            // and more in a group's first stage
+    auto issue = [&](int kt, char* st) __attribute__((always_inline)) {
+        const int left = nb - kt * SB;   // stages past the last load nothing, but keep the count
+        mx.issue(st, kt, left * (A4 ? 16 : 64));
+        mw.issue(st + XB, kt, left * 16);
+    };
+    auto issue_scales = [&](int g) __attribute__((always_inline)) {
+        sw.issue(ssw + (g & 1) * SW::BYTES, g);
+        if constexpr (A4) sx.issue(ssx + (g & 1) * SX::BYTES, g);
+    };
+    // A group's scales in registers, read from LDS at its start: later, the
+    // next group's may be on their way into the other buffer.
+    uint32_t cx[4][SPW][TM], cw[4][SPW][TN];
+    auto read_scales = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int t = 0; t < SPW; ++t) {
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+                    cw[p][t][i] = *reinterpret_cast<const uint8_t*>(ssw + (g & 1) * SW::BYTES + wo[i] + SB * p + 2 * t);
+                if constexpr (A4)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+                        cx[p][t][i] = *reinterpret_cast<const uint8_t*>(ssx + (g & 1) * SX::BYTES + xo[i] + SB * p + 2 * t);
+            }
+    };
+    f32x16 acc[TM][TN] = {};
+    // A wavefront's part of a stage is UNITS fragments deep (a4: 64-k steps,
+    // bf16: 16-k quarters of one); unit u + 1 is read while u multiplies, and the
+    // first before the next stage's loads are issued.
+    constexpr int UNITS = A4 ? SPW : 4 * SPW;
+    u32x4 xf[2][TM], wf[2][TN];   // bf16: wf holds a whole step's codes, in set step % 2
+    // (opaque, so that the compiler keeps to one base and constant offsets, for which it can tell the buffers apart)
+    int xrow = (wm * WM + (A4 ? 0 : wk * SPW * BM)) * 128, wrow = wn * WN * WB;
+    asm volatile("" : "+v"(xrow), "+v"(wrow));
+    auto read_unit = [&](const char* st, auto U) __attribute__((always_inline)) {
+        constexpr int u = decltype(U)::value, t = A4 ? u : u / 4, q = u % 4;
+        const int s = wk * SPW + t;
+        if constexpr (A4 || q == 0) {
+            const int at = wrow + lds_at<WB>(r, 2 * s + half);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) wf[t & 1][j] = *reinterpret_cast<const u32x4*>(st + at + (XB + j * 32 * WB));
+        }
+        const int at = A4 ? xrow + lds_at<128>(r, 2 * s + half) : xrow + lds_at<128>(r, 4 * half + q) + t * (BM * 128);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) xf[u & 1][i] = *reinterpret_cast<const u32x4*>(st + at + i * 4096);
+    };
+    auto compute = [&](int kt, const char* st, auto Slot) __attribute__((always_inline)) {
+        constexpr int p = decltype(Slot)::value;
+        gemm::static_for<UNITS>([&](auto U) {
+            constexpr int u = decltype(U)::value, t = A4 ? u : u / 4, q = u % 4;
+            if constexpr (u + 1 < UNITS) read_unit(st, std::integral_constant<int, u + 1>{});
+            // past K the codes are zeros, whose scale may not be NaN's
+            const bool in = kt * SB + 2 * (wk * SPW + t) + half < nb;
+            if constexpr (A4) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            fp4_operand(xf[u & 1][i]), fp4_operand(wf[t & 1][j]), acc[i][j], 4, 4, 0,
+                            (int)(in ? cx[p][t][i] : 0u), 0, (int)(in ? cw[p][t][j] : 0u));
+            } else {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const bf16x8 w = unpack8(wf[t & 1][j][q], scale_f32(in ? cw[p][t][j] : 0u));
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, xf[u & 1][i]), w,
+                                                                            acc[i][j], 0, 0, 0);
+                }
+            }
+        });
+    };
+    using U0 = std::integral_constant<int, 0>;
+    auto buf = [&](auto Slot) __attribute__((always_inline)) -> char* {
+        constexpr int p = decltype(Slot)::value;
+        if constexpr (p == 0) return st0;
+        else if constexpr (p == 1) return st1;
+        else if constexpr (p == 2) return st2;
+        else return st3;
+    };
+    issue_scales(0);
+    gemm::static_for<NST - 1>([&](auto S) { issue(decltype(S)::value, buf(S)); });
+    auto arrive = [&](auto Allowed) __attribute__((always_inline)) {
+        wait_vmcnt<decltype(Allowed)::value>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // stage landed; the previous one is read
+    };
+    int kt = 0;
+    for (; kt + NST <= nk; kt += NST)
+        gemm::static_for<NST>([&](auto S) {
+            constexpr int p = decltype(S)::value;
+            using Prev = std::integral_constant<int, (p + NST - 1) % NST>;
+            arrive(std::integral_constant<int, (NST - 2) * LPW + (p == 1 || p == 2 ? SPG : 0)>{});
+            if constexpr (p == 0) {
+                read_scales(kt >> 2);
+                read_unit(buf(S), U0{});
+                __builtin_amdgcn_sched_barrier(0);
+                issue_scales((kt >> 2) + 1);
+            } else {
+                read_unit(buf(S), U0{});
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            issue(kt + p + NST - 1, buf(Prev{}));
+            compute(kt + p, buf(S), S);
+        });
+    gemm::static_for<NST - 1>([&](auto S) {   // the stages left, all loaded already
+        constexpr int p = decltype(S)::value;
+        if (kt + p < nk) {
+            arrive(std::integral_constant<int, (NST - 2 - p) * LPW>{});
+            if constexpr (p == 0) read_scales(kt >> 2);
+            read_unit(buf(S), U0{});
+            compute(kt + p, buf(S), S);
+        }
+    });
+    wait_vmcnt<0>();
+
+    // Half a block at a time through LDS: every set's sums, then all threads add
+    // the sets' in order and write four neighbouring outputs at a time.
+    constexpr int THREADS = NWK * 64, PER = (128 + THREADS - 1) / THREADS;   // 16 x 32 outputs, four each
+    float* red = reinterpret_cast<float*>(st0);
+    const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (BF16 ? 7 : 15)) == 0;
+    const int set = wm * NWN + wn;
+    gemm::static_for<2 * TM * TN>([&](auto B) {
+        constexpr int b = decltype(B)::value / 2, h = decltype(B)::value % 2, i = b / TN, j = b % TN;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            red[((set * NWK + wk) * 16 + 8 * (e >> 2) + 4 * half + (e & 3)) * 36 + r] = acc[i][j][8 * h + e];
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int t = (q * NWK + wk) * 64 + lane, row = t >> 3, c = (t & 7) * 4;
+            const int64_t m = m0 + wm * WM + i * 32 + h * 16 + row, n = n0 + wn * WN + j * 32 + c;
+            if (row >= 16 || m >= a.M || n >= a.N) continue;
+            f32x4 v = *reinterpret_cast<const f32x4*>(red + (set * NWK * 16 + row) * 36 + c);
+#pragma unroll
+            for (int w = 1; w < NWK; ++w) v += *reinterpret_cast<const f32x4*>(red + ((set * NWK + w) * 16 + row) * 36 + c);
+            if (wide) {
+                if constexpr (BF16)
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + m * a.N + n) =
+                        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                else
+                    *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + m * a.N + n) = v;
+            } else {
+                for (int k = 0; k < 4; ++k)
+                    if (n + k < a.N) store_y<BF16>(a.y, m * a.N + n + k, v[k]);
+            }
+        }
+    });
+}
+
+template <bool A4, int BM, int BN, int NWM, int NWN, int NWK>
+void launch_ring(const MxGemmArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN))), block(NWM * NWN * NWK * 64);
+    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, false>), grid, block, 0, stream, a);
+}
+
 template <bool A4, int MB, int RT, int NW, int NPW>
 void launch_skinny(const MxGemmArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)(((a.N + 16 * RT - 1) / (16 * RT)) * ((a.M + 16 * MB - 1) / (16 * MB)))), block(64 * NW);
@@ -608,20 +885,52 @@ void launch_a16_tile(const MxGemmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+static int cfg() { const char* e = getenv("MXC"); return e ? atoi(e) : -1; }
 hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
+    switch (cfg()) {
+    case 0: launch_skinny<false, 1, 1, 16, 2>(a, stream); break;
+    case 1: launch_skinny<false, 2, 1, 16, 1>(a, stream); break;
+    case 2: launch_skinny<false, 4, 1, 8, 1>(a, stream); break;
+    case 3: launch_a16_tile<256, 256, 2, 4>(a, stream); break;
+    case 4: launch_ring<false, 64, 64, 1, 2, 2>(a, stream); break;
+    case 5: launch_ring<false, 64, 64, 2, 1, 2>(a, stream); break;
+    case 6: launch_ring<false, 64, 128, 1, 2, 2>(a, stream); break;
+    case 7: launch_ring<false, 64, 128, 2, 2, 2>(a, stream); break;
+    case 9: launch_ring<false, 32, 64, 1, 2, 2>(a, stream); break;
+    case 10: launch_ring<false, 32, 128, 1, 2, 2>(a, stream); break;
+    case 11: launch_ring<false, 128, 64, 2, 1, 2>(a, stream); break;
+    case 13: launch_ring<false, 64, 64, 2, 2, 1>(a, stream); break;
+    default:
     if (a.M <= 16) launch_skinny<false, 1, 1, 16, 2>(a, stream);
     else if (a.M <= 32) launch_skinny<false, 2, 1, 16, 1>(a, stream);
     else if (a.M <= 64 || a.N >= kMxTileMaxN) launch_skinny<false, 4, 1, 8, 1>(a, stream);
     else launch_a16_tile<256, 256, 2, 4>(a, stream);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
+    switch (cfg()) {
+    case 0: launch_skinny<true, 1, 1, 16, 2>(a, stream); break;
+    case 1: launch_skinny<true, 2, 1, 16, 2>(a, stream); break;
+    case 2: launch_skinny<true, 4, 1, 16, 1>(a, stream); break;
+    case 3: launch_a4_tile<256, 256, 2, 4>(a, stream); break;
+    case 4: launch_ring<true, 64, 64, 1, 1, 4>(a, stream); break;
+    case 5: launch_ring<true, 64, 64, 2, 2, 2>(a, stream); break;
+    case 6: launch_ring<true, 64, 128, 1, 2, 2>(a, stream); break;
+    case 7: launch_ring<true, 64, 128, 1, 2, 4>(a, stream); break;
+    case 8: launch_ring<true, 128, 128, 2, 2, 2>(a, stream); break;
+    case 9: launch_ring<true, 32, 64, 1, 1, 4>(a, stream); break;
+    case 10: launch_ring<true, 32, 128, 1, 1, 4>(a, stream); break;
+    case 11: launch_ring<true, 32, 32, 1, 1, 4>(a, stream); break;
+    case 12: launch_ring<true, 128, 128, 2, 2, 1>(a, stream); break;
+    case 13: launch_ring<true, 64, 64, 2, 2, 1>(a, stream); break;
+    default:
     if (a.M <= 16) launch_skinny<true, 1, 1, 16, 2>(a, stream);
     else if (a.M <= 32) launch_skinny<true, 2, 1, 16, 2>(a, stream);
     else if (a.M <= 64 || a.K < 256 || a.N >= kMxTileMaxN) launch_skinny<true, 4, 1, 16, 1>(a, stream);
-    else if (getenv("MXC") && atoi(getenv("MXC"))==1) launch_a4_tile<256, 256, 2, 2>(a, stream);
     else launch_a4_tile<256, 256, 2, 4>(a, stream);
+    }
     return hipGetLastError();
 }
 
