@@ -6,7 +6,6 @@
 //
 // K is a multiple of 32, so a 16-byte piece of packed codes is one block.
 #include <type_traits>
-#include <cstdlib>
 
 #include "ar_internal.h"
 #include "gemm_tiles.h"
@@ -67,132 +66,74 @@ __device__ __forceinline__ void mx_tile(uint32_t tiles_m, uint32_t tiles_n, uint
 }
 
 // ------------------------------------------------------- few rows of X ----
-// Streaming the weight once is the bound.  No LDS staging; a
-// workgroup of NW wavefronts owns 16 RT weight rows and its wavefronts take
-// the super-steps of 128 k in turn (wave w: w, w + NW, ...), NPW of them per
-// round with all loads issued first.  Partial sums meet in LDS in wave order.
-// A lane holds row l % 16 and block c = l / 16 of the super-step: 16 bytes of
-// codes and one scale byte.  The bf16 form's four MFMAs of 32 k take the k of
-// a lane's block in order (lane group c, MFMA j: k = 32 c + 8 j), the same
-// for both operands.
-template <bool A4, bool BF16, int MB, int RT, int NW, int NPW>
-__global__ void __launch_bounds__(64 * NW) mx_gemm_skinny_kernel(MxGemmArgs a) {
-    __shared__ float red[NW][MB][RT][16][17];
+// Up to 16 rows: streaming the weight once is the bound.  No LDS staging; a
+// workgroup of 16 wavefronts owns 16 weight rows and its wavefronts take the
+// super-steps of 128 k in turn, two per round with all loads issued first.
+// Partial sums meet in LDS in wave order.  A lane holds row l % 16 and block
+// c = l / 16 of the super-step: 16 bytes of codes and one scale byte.  The bf16
+// form's four MFMAs of 32 k take the k of a lane's block in order (lane group
+// c, MFMA j: k = 32 c + 8 j), the same for both operands.
+// Rows past M or N are clamped and their results not stored.
+template <bool A4, bool BF16>
+__global__ void __launch_bounds__(1024) mx_gemm_skinny_kernel(MxGemmArgs a) {
+    constexpr int NW = 16, NPW = 2, XJ = A4 ? 1 : 4;
+    __shared__ float red[NW][16][17];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r16 = lane & 15, c = lane >> 4;
-    const int64_t tiles_n = (a.N + 16 * RT - 1) / (16 * RT), tile_m = blockIdx.x / tiles_n;
-    const int64_t n0 = (blockIdx.x - tile_m * tiles_n) * 16 * RT, m0 = tile_m * 16 * MB;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int nb = (int)(a.K >> 5);            // blocks of a row
     const int nss = (nb + 3) >> 2;             // super-steps
-    const uint8_t *wrow[RT], *wsc[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        int64_t n = n0 + rt * 16 + r16;
-        if (n >= a.N) n = a.N - 1;
-        wrow[rt] = a.wp + n * (a.K >> 1);
-        wsc[rt] = a.ws + n * nb;
-    }
-    const uint8_t *xrow[MB], *xsc[MB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-        int64_t m = m0 + mb * 16 + r16;
-        if (m >= a.M) m = a.M - 1;
-        if constexpr (A4) {
-            xrow[mb] = a.xp + m * (a.K >> 1);
-            xsc[mb] = a.xs + m * nb;
-        } else {
-            xrow[mb] = reinterpret_cast<const uint8_t*>(a.x + m * a.K);
-        }
-    }
-    f32x4 acc[MB][RT];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) acc[mb][rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    constexpr int XJ = A4 ? 1 : 4;
+    const int64_t n = n0 + r16 < a.N ? n0 + r16 : a.N - 1, m = r16 < a.M ? r16 : a.M - 1;
+    const uint8_t *wrow = a.wp + n * (a.K >> 1), *wsc = a.ws + n * nb;
+    const uint8_t* xrow = A4 ? a.xp + m * (a.K >> 1) : reinterpret_cast<const uint8_t*>(a.x + m * a.K);
+    const uint8_t* xsc = a.xs + m * nb;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int base = wave; base < nss; base += NW * NPW) {
-        u32x4 w[NPW][RT], x[NPW][MB][XJ];
-        uint32_t ws[NPW][RT], xs[NPW][MB];
+        u32x4 w[NPW], x[NPW][XJ];
+        uint32_t ws[NPW], xs[NPW];
 #pragma unroll
         for (int i = 0; i < NPW; ++i) {
             const int b = (base + NW * i) * 4 + c;   // this lane's block
-            const bool in = b < nb;
-            const int64_t bb = in ? b : 0;
+            const int64_t in = b < nb ? b : 0;
+            w[i] = *reinterpret_cast<const u32x4*>(wrow + in * 16);
+            ws[i] = wsc[in];
+            if constexpr (A4) xs[i] = xsc[in];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                w[i][rt] = *reinterpret_cast<const u32x4*>(wrow[rt] + bb * 16);
-                ws[i][rt] = wsc[rt][bb];
-            }
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                if constexpr (A4) {
-                    x[i][mb][0] = *reinterpret_cast<const u32x4*>(xrow[mb] + bb * 16);
-                    xs[i][mb] = xsc[mb][bb];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[i][mb][j] = *reinterpret_cast<const u32x4*>(xrow[mb] + bb * 64 + 16 * j);
-                }
-            }
+            for (int j = 0; j < XJ; ++j) x[i][j] = *reinterpret_cast<const u32x4*>(xrow + in * (16 * XJ) + 16 * j);
         }
 #pragma unroll
         for (int i = 0; i < NPW; ++i) {
             const int ss = base + NW * i;
             if (ss >= nss) break;
             if (ss * 4 + 4 > nb) {   // the last super-step of a K that is no multiple of 128
-                const bool in = ss * 4 + c < nb;
+                const uint32_t keep = ss * 4 + c < nb ? ~0u : 0u;
+                w[i] &= keep;
+                ws[i] &= keep;
+                if constexpr (A4) xs[i] &= keep;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    w[i][rt] = in ? w[i][rt] : u32x4{0u, 0u, 0u, 0u};
-                    ws[i][rt] = in ? ws[i][rt] : 0u;
-                }
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-#pragma unroll
-                    for (int j = 0; j < XJ; ++j) x[i][mb][j] = in ? x[i][mb][j] : u32x4{0u, 0u, 0u, 0u};
-                    if constexpr (A4) xs[i][mb] = in ? xs[i][mb] : 0u;
-                }
+                for (int j = 0; j < XJ; ++j) x[i][j] &= keep;
             }
             if constexpr (A4) {
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        acc[mb][rt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            fp4_operand(x[i][mb][0]), fp4_operand(w[i][rt]), acc[mb][rt], 4, 4, 0, (int)xs[i][mb], 0,
-                            (int)ws[i][rt]);
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(x[i][0]), fp4_operand(w[i]), acc, 4, 4,
+                                                                       0, (int)xs[i], 0, (int)ws[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const bf16x8 wf = unpack8(w[i][rt][j], scale_f32(ws[i][rt]));
-#pragma unroll
-                        for (int mb = 0; mb < MB; ++mb)
-                            acc[mb][rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8, x[i][mb][j]), wf, acc[mb][rt], 0, 0, 0);
-                    }
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[i][j]),
+                                                                  unpack8(w[i][j], scale_f32(ws[i])), acc, 0, 0, 0);
             }
         }
     }
     // C of a 16 x 16 MFMA: lane l, element r -> row 4 (l / 16) + r, column l % 16
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) red[wave][mb][rt][4 * c + r][r16] = acc[mb][rt][r];
+    for (int r = 0; r < 4; ++r) red[wave][4 * c + r][r16] = acc[r];
     __syncthreads();
-    for (int t = threadIdx.x; t < MB * 256 * RT; t += 64 * NW) {
-        const int j = t % 16, rt = (t / 16) % RT, i = (t / (16 * RT)) % 16, mb = t / (256 * RT);
-        const int64_t m = m0 + mb * 16 + i, n = n0 + rt * 16 + j;
-        if (m >= a.M || n >= a.N) continue;
-        float sum = red[0][mb][rt][i][j];
+    const int i = threadIdx.x / 16, j = threadIdx.x % 16;
+    if (threadIdx.x >= 256 || i >= a.M || n0 + j >= a.N) return;
+    float sum = red[0][i][j];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) sum += red[w][mb][rt][i][j];
-        store_y<BF16>(a.y, m * a.N + n, sum);
-    }
+    for (int w = 1; w < NW; ++w) sum += red[w][i][j];
+    store_y<BF16>(a.y, i * a.N + n0 + j, sum);
 }
 
 // ------------------------------------------------------ many rows of X ----
@@ -478,100 +419,6 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmA
     store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
 }
 
-// bf16 activations: a stage is 64 k, 128 bytes of an X row and 32 of a W row.
-// A lane's 16 bytes of codes are one block (half l / 32 of the stage), which
-// the stage's four MFMAs of 16 k take in order (lane half h, MFMA j: k = 32 h
-// + 8 j, the same for X); it is unpacked in registers with the lane's one
-// scale byte, fetched a stage ahead.  Where K ends in half a stage, the upper
-// lanes multiply zeros there.
-template <int BM, int BN, int NWM, int NWN, bool BF16>
-__global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a16_tile_kernel(MxGemmArgs a) {
-    constexpr int NW = NWM * NWN, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32;
-    __shared__ __attribute__((aligned(1024))) char sx0[BM * 128], sw0[BN * 32], sx1[BM * 128], sw1[BN * 32];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / NWN, wn = wave % NWN, r = lane & 31, half = lane >> 5;
-    uint32_t tile_m, tile_n;
-    mx_tile((uint32_t)((a.M + BM - 1) / BM), (uint32_t)((a.N + BN - 1) / BN), tile_m, tile_n);
-    const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
-    const int nb = (int)(a.K >> 5), nk = (nb + 1) >> 1;
-
-    Mover<BM, 128, NW> mx;
-    Mover<BN, 32, NW> mw;
-    mx.init(a.x, m0, a.M, 2 * a.K, wave);
-    mw.init(a.wp, n0, a.N, a.K >> 1, wave);
-    const uint8_t* ws = a.ws + n0 * nb;
-    uint32_t wo[TN], nw[TN];
-#pragma unroll
-    for (int i = 0; i < TN; ++i) wo[i] = row_offset(n0, wn * WN + i * 32 + r, a.N, nb);
-    auto load_scales = [&](int kt) __attribute__((always_inline)) {
-        const int b = 2 * kt + half;
-#pragma unroll
-        for (int i = 0; i < TN; ++i) nw[i] = ws[wo[i] + (uint32_t)(b < nb ? b : nb - 1)];
-    };
-    f32x16 acc[TM][TN] = {};
-    mx.issue(sx0, 0);
-    mw.issue(sw0, 0);
-    load_scales(0);
-
-    // CUT: only the lower half of the stage is within K
-    auto stage = [&](int kt, const char* X, const char* W, char* nextX, char* nextW, auto cut)
-                     __attribute__((always_inline)) {
-        constexpr bool CUT = decltype(cut)::value;
-        const uint32_t keep = CUT && half ? 0u : ~0u;
-        wait_vmcnt<0>();
-        lds_barrier();
-        float sc[TN];
-#pragma unroll
-        for (int i = 0; i < TN; ++i) sc[i] = scale_f32(nw[i]);
-        u32x4 codes[TN], xf[2][TM];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            codes[j] = *reinterpret_cast<const u32x4*>(W + lds_at<32>(wn * WN + j * 32 + r, half));
-            if constexpr (CUT) codes[j] &= keep;
-        }
-        auto frags = [&](auto S) __attribute__((always_inline)) {
-            constexpr int s = decltype(S)::value;
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                xf[s & 1][i] = *reinterpret_cast<const u32x4*>(X + lds_at<128>(wm * WM + i * 32 + r, 4 * half + s));
-                if constexpr (CUT) xf[s & 1][i] &= keep;
-            }
-        };
-        frags(std::integral_constant<int, 0>{});
-        if constexpr (!CUT) {
-            const int next = kt + 1 < nk ? kt + 1 : kt;   // the stage past the last repeats it: read by no one
-            mx.issue(nextX, next);
-            mw.issue(nextW, next);
-            load_scales(next);
-        }
-        gemm::static_for<4>([&](auto S) {
-            constexpr int s = decltype(S)::value;
-            if constexpr (s < 3) frags(std::integral_constant<int, s + 1>{});
-            bf16x8 wf[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) wf[j] = unpack8(codes[j][s], sc[j]);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, xf[s & 1][i]), wf[j],
-                                                                        acc[i][j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        });
-    };
-    const int whole = nb >> 1;
-    int kt = 0;
-    for (; kt + 2 <= whole; kt += 2) {
-        stage(kt, sx0, sw0, sx1, sw1, std::false_type{});
-        stage(kt + 1, sx1, sw1, sx0, sw0, std::false_type{});
-    }
-    if (kt < whole) stage(kt, sx0, sw0, sx1, sw1, std::false_type{});
-    if (nb & 1) stage(whole, whole & 1 ? sx1 : sx0, whole & 1 ? sw1 : sw0, nullptr, nullptr, std::true_type{});
-    wait_vmcnt<0>();   // the last, unread loads into LDS
-
-    store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
-}
-
 // --------------------------------------------------- a few hundred rows ----
 // Tiles too small for a wavefront to own a full K: NWM x NWN wavefronts cover
 // BM x BN outputs and NWK such sets split every stage between them; their sums
@@ -583,8 +430,9 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a16_tile_kernel(MxGemm
 template <int ROWS, int RB, int SUB, int NW>
 struct RingMover {
     // LDS row s * ROWS + r holds bytes [RB s, RB s + RB) of row r's stage
-    static constexpr int SLOTS = RB / 16, RPI = 64 / SLOTS, Q = ROWS * SUB / RPI / NW;
-    static_assert(Q * RPI * NW == ROWS * SUB, "rows must split evenly over the wavefronts");
+    // Q instructions per wavefront; with fewer than NW pieces of 1 KB some are moved twice, to the same place
+    static constexpr int SLOTS = RB / 16, RPI = 64 / SLOTS, ALL = ROWS * SUB / RPI, Q = (ALL + NW - 1) / NW;
+    static_assert(ALL * RPI == ROWS * SUB, "rows must fill whole instructions");
     __amdgpu_buffer_rsrc_t rsrc;
     uint32_t off[Q];
     uint32_t col[Q];   // byte of the row's stage
@@ -598,7 +446,7 @@ struct RingMover {
             left < 0xFFFFFFF0ll ? (int)left : (int)0xFFFFFFF0, 0x00020000);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const int lr = (q * NW + w) * RPI + lane / SLOTS, s = lr / ROWS, r = lr % ROWS;
+            const int lr = (q * NW + w) % ALL * RPI + lane / SLOTS, s = lr / ROWS, r = lr % ROWS;
             col[q] = (uint32_t)(s * RB + (((lane % SLOTS) ^ ((lr / (256 / RB)) % SLOTS)) << 4));
             off[q] = (uint32_t)r * (uint32_t)pitch + col[q];
         }
@@ -608,8 +456,8 @@ struct RingMover {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const uint32_t o = (int)col[q] < left ? off[q] + (uint32_t)(kt * RB * SUB) : 0xFFFFFFF0u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (q * NW + wave) * 1024), 16, (int)o, 0, 0,
-                                                     0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (q * NW + wave) % ALL * 1024), 16, (int)o,
+                                                     0, 0, 0);
         }
     }
 };
@@ -654,10 +502,10 @@ struct ScaleRing {
     }
 };
 
-template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, bool BF16>
+template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB, bool BF16>
 __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGemmArgs a) {
     constexpr int NW = NWM * NWN * NWK, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32;
-    constexpr int NST = 4, SB = A4 ? 8 : 4, XSUB = A4 ? 1 : 2, STEPS = SB / 2, SPW = STEPS / NWK;
+    constexpr int NST = 4, XSUB = A4 ? 1 : SB / 2, STEPS = SB / 2, SPW = STEPS / NWK;
     constexpr int WB = SB * 16, XB = XSUB * BM * 128;
     constexpr int RED = NW * 16 * 36 * 4;   // half a block of every wavefront
     constexpr int STAGE = XB + BN * WB > RED ? XB + BN * WB : RED;
@@ -690,14 +538,17 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
 
     constexpr int LPW = decltype(mx)::Q + decltype(mw)::Q;   // loads per wavefront and stage
     constexpr int SPG = SW::S + (A4 ? SX::S : 0);            // and more in a group's first stage
+    const int rot = nk % 4 == 0 ? (int)(tile_n % (uint32_t)(nk / 4)) * 4 : 0;
+    auto turned = [&](int kt) { const int k = kt + rot; return k < nk ? k : k - nk; };
     auto issue = [&](int kt, char* st) __attribute__((always_inline)) {
-        const int left = nb - kt * SB;   // stages past the last load nothing, but keep the count
-        mx.issue(st, kt, left * (A4 ? 16 : 64));
-        mw.issue(st + XB, kt, left * 16);
+        const int kk = turned(kt), left = kt < nk ? nb - kk * SB : 0;   // stages past the last load nothing, but keep the count
+        mx.issue(st, kk, left * (A4 ? 16 : 64));
+        mw.issue(st + XB, kk, left * 16);
     };
     auto issue_scales = [&](int g) __attribute__((always_inline)) {
-        sw.issue(ssw + (g & 1) * SW::BYTES, g);
-        if constexpr (A4) sx.issue(ssx + (g & 1) * SX::BYTES, g);
+        const int gg = turned(4 * g) >> 2;
+        sw.issue(ssw + (g & 1) * SW::BYTES, gg);
+        if constexpr (A4) sx.issue(ssx + (g & 1) * SX::BYTES, gg);
     };
     // A group's scales in registers, read from LDS at its start: later, the
     // next group's may be on their way into the other buffer.
@@ -743,7 +594,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
             constexpr int u = decltype(U)::value, t = A4 ? u : u / 4, q = u % 4;
             if constexpr (u + 1 < UNITS) read_unit(st, std::integral_constant<int, u + 1>{});
             // past K the codes are zeros, whose scale may not be NaN's
-            const bool in = kt * SB + 2 * (wk * SPW + t) + half < nb;
+            const bool in = turned(kt) * SB + 2 * (wk * SPW + t) + half < nb;
             if constexpr (A4) {
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
@@ -842,95 +693,67 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
     });
 }
 
-template <bool A4, int BM, int BN, int NWM, int NWN, int NWK>
+template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB>
 void launch_ring(const MxGemmArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN))), block(NWM * NWN * NWK * 64);
-    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, false>), grid, block, 0, stream, a);
+    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, SB, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, SB, false>), grid, block, 0, stream, a);
 }
 
-template <bool A4, int MB, int RT, int NW, int NPW>
+template <bool A4>
 void launch_skinny(const MxGemmArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(((a.N + 16 * RT - 1) / (16 * RT)) * ((a.M + 16 * MB - 1) / (16 * MB)))), block(64 * NW);
-    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_skinny_kernel<A4, true, MB, RT, NW, NPW>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((mx_gemm_skinny_kernel<A4, false, MB, RT, NW, NPW>), grid, block, 0, stream, a);
+    const dim3 grid((unsigned)((a.N + 15) / 16));
+    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_skinny_kernel<A4, true>), grid, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((mx_gemm_skinny_kernel<A4, false>), grid, dim3(1024), 0, stream, a);
 }
 
-template <int BM, int BN>
-dim3 tile_grid(const MxGemmArgs& a) {
-    return dim3((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN)));
-}
-template <int BM, int BN, int NWM, int NWN, bool BF16>
-void launch_a4_tile_y(const MxGemmArgs& a, hipStream_t stream) {
-    const dim3 grid = tile_grid<BM, BN>(a), block(NWM * NWN * 64);
-    const bool aligned = ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
-    if (a.K % 128 == 0 && aligned)
-        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, BF16, true>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, NWM, NWN, BF16, false>), grid, block, 0, stream, a);
-}
-template <int BM, int BN, int NWM, int NWN>
+int64_t tiles(const MxGemmArgs& a, int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); }
+
 void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
-    if (a.y_bf16) launch_a4_tile_y<BM, BN, NWM, NWN, true>(a, stream);
-    else launch_a4_tile_y<BM, BN, NWM, NWN, false>(a, stream);
-}
-template <int BM, int BN, int NWM, int NWN>
-void launch_a16_tile(const MxGemmArgs& a, hipStream_t stream) {
-    const dim3 block(NWM * NWN * 64);
-    if (a.y_bf16)
-        hipLaunchKernelGGL((mx_gemm_a16_tile_kernel<BM, BN, NWM, NWN, true>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((mx_gemm_a16_tile_kernel<BM, BN, NWM, NWN, false>), (tile_grid<BM, BN>(a)), block, 0, stream, a);
+    const dim3 grid((unsigned)tiles(a, 256, 256)), block(512);
+    const bool grouped = a.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
+    if (a.y_bf16) {
+        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, true, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, true, false>), grid, block, 0, stream, a);
+    } else {
+        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, false, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, false, false>), grid, block, 0, stream, a);
+    }
 }
 
 }  // namespace
 
-static int cfg() { const char* e = getenv("MXC"); return e ? atoi(e) : -1; }
+// The tile is the smallest that does not need more workgroups than the 256
+// CUs, otherwise the largest: a workgroup's time is that of its K loop, most of
+// it latency, so one round of small tiles beats a part-filled round of large
+// ones, and with several rounds what counts is how often a tile re-reads its
+// operands.  Measured (us, bf16 X | packed X; smaller and larger neighbour):
+//   16 x 28672 x 8192:  32x128 36, 32x64 39, 64x128 41 | 32x64 27, 32x32 31, 32x128 32
+//   64 x 4096 x 4096:   32x64 10, 64x64 13 | 32x32 6.0, 32x64 7.4
+//   130 x 4096 x 11008: 64x64 29, 32x64 33, 64x128 39 | 64x64 16, 32x64 20, 64x128 21
+//   512 x 11008 x 4096: 128x256 56, 64x128 58 | 256x256 28, 128x128 31, 64x128 33
+// Up to 16 rows on up to 4096 outputs (one workgroup of 16 a CU) take the
+// skinny kernel, which has no ring to fill: 1 x 4096 x 11008 9.4 against 24 |
+// 7.9 against 11.
 hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
-    switch (cfg()) {
-    case 0: launch_skinny<false, 1, 1, 16, 2>(a, stream); break;
-    case 1: launch_skinny<false, 2, 1, 16, 1>(a, stream); break;
-    case 2: launch_skinny<false, 4, 1, 8, 1>(a, stream); break;
-    case 3: launch_a16_tile<256, 256, 2, 4>(a, stream); break;
-    case 4: launch_ring<false, 64, 64, 1, 2, 2>(a, stream); break;
-    case 5: launch_ring<false, 64, 64, 2, 1, 2>(a, stream); break;
-    case 6: launch_ring<false, 64, 128, 1, 2, 2>(a, stream); break;
-    case 7: launch_ring<false, 64, 128, 2, 2, 2>(a, stream); break;
-    case 9: launch_ring<false, 32, 64, 1, 2, 2>(a, stream); break;
-    case 10: launch_ring<false, 32, 128, 1, 2, 2>(a, stream); break;
-    case 11: launch_ring<false, 128, 64, 2, 1, 2>(a, stream); break;
-    case 13: launch_ring<false, 64, 64, 2, 2, 1>(a, stream); break;
-    default:
-    if (a.M <= 16) launch_skinny<false, 1, 1, 16, 2>(a, stream);
-    else if (a.M <= 32) launch_skinny<false, 2, 1, 16, 1>(a, stream);
-    else if (a.M <= 64 || a.N >= kMxTileMaxN) launch_skinny<false, 4, 1, 8, 1>(a, stream);
-    else launch_a16_tile<256, 256, 2, 4>(a, stream);
-    }
+    if (a.M <= 16 && a.N <= 4096) launch_skinny<false>(a, stream);
+    else if (tiles(a, 32, 64) <= 256) launch_ring<false, 32, 64, 1, 2, 2, 4>(a, stream);
+    else if (a.M <= 32) launch_ring<false, 32, 128, 1, 2, 2, 4>(a, stream);
+    else if (tiles(a, 64, 64) <= 256) launch_ring<false, 64, 64, 1, 2, 2, 4>(a, stream);
+    else if (tiles(a, 64, 128) <= 256) launch_ring<false, 64, 128, 2, 2, 2, 4>(a, stream);
+    else launch_ring<false, 128, 256, 2, 4, 1, 2>(a, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
-    switch (cfg()) {
-    case 0: launch_skinny<true, 1, 1, 16, 2>(a, stream); break;
-    case 1: launch_skinny<true, 2, 1, 16, 2>(a, stream); break;
-    case 2: launch_skinny<true, 4, 1, 16, 1>(a, stream); break;
-    case 3: launch_a4_tile<256, 256, 2, 4>(a, stream); break;
-    case 4: launch_ring<true, 64, 64, 1, 1, 4>(a, stream); break;
-    case 5: launch_ring<true, 64, 64, 2, 2, 2>(a, stream); break;
-    case 6: launch_ring<true, 64, 128, 1, 2, 2>(a, stream); break;
-    case 7: launch_ring<true, 64, 128, 1, 2, 4>(a, stream); break;
-    case 8: launch_ring<true, 128, 128, 2, 2, 2>(a, stream); break;
-    case 9: launch_ring<true, 32, 64, 1, 1, 4>(a, stream); break;
-    case 10: launch_ring<true, 32, 128, 1, 1, 4>(a, stream); break;
-    case 11: launch_ring<true, 32, 32, 1, 1, 4>(a, stream); break;
-    case 12: launch_ring<true, 128, 128, 2, 2, 1>(a, stream); break;
-    case 13: launch_ring<true, 64, 64, 2, 2, 1>(a, stream); break;
-    default:
-    if (a.M <= 16) launch_skinny<true, 1, 1, 16, 2>(a, stream);
-    else if (a.M <= 32) launch_skinny<true, 2, 1, 16, 2>(a, stream);
-    else if (a.M <= 64 || a.K < 256 || a.N >= kMxTileMaxN) launch_skinny<true, 4, 1, 16, 1>(a, stream);
-    else launch_a4_tile<256, 256, 2, 4>(a, stream);
-    }
+    if (a.M <= 16 && a.N <= 4096) launch_skinny<true>(a, stream);
+    else if (tiles(a, 32, 32) <= 256) launch_ring<true, 32, 32, 1, 1, 4, 8>(a, stream);
+    else if (tiles(a, 32, 64) <= 256 || a.M <= 32) launch_ring<true, 32, 64, 1, 1, 4, 8>(a, stream);
+    else if (tiles(a, 64, 64) <= 256) launch_ring<true, 64, 64, 1, 1, 4, 8>(a, stream);
+    else if (tiles(a, 64, 128) <= 256) launch_ring<true, 64, 128, 1, 2, 2, 8>(a, stream);
+    else if (tiles(a, 128, 128) <= 256 || a.K < 256 || a.N >= kMxTileMaxN)
+        launch_ring<true, 128, 128, 2, 2, 2, 8>(a, stream);
+    else launch_a4_tile(a, stream);
     return hipGetLastError();
 }
 
