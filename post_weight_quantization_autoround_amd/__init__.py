@@ -172,7 +172,13 @@ def _opt(t, name, dtype, shape):
     return None if t is None else _dev(t, name, dtype, shape)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream() -> int:
+    # the handle of torch.cuda.current_stream(), whose Stream object costs most of 3 us a call
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -266,27 +272,31 @@ def w4a16_gemm(X: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, zero:
 
 
 # ------------------------------------------------------------ packed MXFP4
-def _mx_in(t, name, dtypes, shape=None, strided=False):
-    """Checks an input of the MXFP4 calls: on the current HIP device, one of
-    `dtypes`, `shape`, contiguous (`strided`: rows may lie apart)."""
+def _mx_in(t, name, dtypes, dev, shape=None, strided=False):
+    """Data pointer of an input of the MXFP4 calls, which is on the current HIP
+    device `dev`, of one of `dtypes`, of `shape` (two dimensions without one)
+    and contiguous (`strided`: its rows are)."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev and t.dtype in dtypes
+            and (t.dim() == 2 if shape is None else t.shape == shape)
+            and (t.is_contiguous() or (strided and (t.shape[1] <= 1 or t.stride(1) == 1)))):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a HIP device, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dim() != 2 and shape is None:
+    if shape is None and t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    if strided:
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have contiguous rows")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must {'have contiguous rows' if strided else 'be contiguous'}")
+
+
+def _mx_dev():
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
 
 
 _F32_BF16 = (torch.float32, torch.bfloat16)
@@ -295,11 +305,11 @@ _F32 = (torch.float32,)
 _U8 = (torch.uint8,)
 
 
-def _mx_out(rows, k, dev):
+def _mx_out(rows, k, like):
     if k % 32 != 0:
         raise ValueError(f"the last dimension must be a multiple of 32 (the MXFP4 block), got {k}")
-    return (torch.empty((rows, k // 2), dtype=torch.uint8, device=dev),
-            torch.empty((rows, k // 32), dtype=torch.uint8, device=dev))
+    return (like.new_empty((rows, k // 2), dtype=torch.uint8),
+            like.new_empty((rows, k // 32), dtype=torch.uint8))
 
 
 def pack_mxfp4(W: torch.Tensor, alpha: torch.Tensor | None = None):
@@ -308,20 +318,22 @@ def pack_mxfp4(W: torch.Tensor, alpha: torch.Tensor | None = None):
     exponent + 127, 255 for a block without a finite maximum).  The codes are
     those of qdq_rtn(fmt=AR_FMT_MXFP4, bits=4, group_size=32, alpha=alpha);
     alpha [N, K/32] clips the block maxima."""
-    pw = _mx_in(W, "W", _F32_BF16)
+    dev = _mx_dev()
+    pw = _mx_in(W, "W", _F32_BF16, dev)
     N, K = W.shape
-    packed, scale = _mx_out(N, K, W.device)
-    pa = None if alpha is None else _mx_in(alpha, "alpha", _F32, scale.shape)
+    packed, scale = _mx_out(N, K, W)
+    pa = None if alpha is None else _mx_in(alpha, "alpha", _F32, dev, scale.shape)
     _check(lib.ar_pack_mxfp4(pw, _dtype_code(W), N, K, pa, packed.data_ptr(), scale.data_ptr(), _stream()))
     return packed, scale
 
 
 def unpack_mxfp4(packed: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.float32):
     """The values [N, K] of packed MXFP4, fp32 or bf16."""
-    pp = _mx_in(packed, "packed", _U8)
+    dev = _mx_dev()
+    pp = _mx_in(packed, "packed", _U8, dev)
     N, K = packed.shape[0], 2 * packed.shape[1]
-    ps = _mx_in(scale, "scale", _U8, (N, K // 32))
-    out = torch.empty((N, K), dtype=out_dtype, device=packed.device)
+    ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
+    out = packed.new_empty((N, K), dtype=out_dtype)
     _check(lib.ar_unpack_mxfp4(pp, ps, N, K, out.data_ptr(), _dtype_code(out), _stream()))
     return out
 
@@ -332,11 +344,12 @@ def rmsnorm_mxfp4(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
     delta_scale * delta; x bf16 [M, H], delta bf16 or fp32 [M, H], weight fp32
     [H] or None (= 1).  Returns (packed, scale, r) with r the bf16 residual
     stream, None without a delta (r is x then)."""
-    px = _mx_in(x, "x", _BF16)
+    dev = _mx_dev()
+    px = _mx_in(x, "x", _BF16, dev)
     M, H = x.shape
-    pd = None if delta is None else _mx_in(delta, "delta", _F32_BF16, x.shape)
-    pw = None if weight is None else _mx_in(weight, "weight", _F32, (H,))
-    packed, scale = _mx_out(M, H, x.device)
+    pd = None if delta is None else _mx_in(delta, "delta", _F32_BF16, dev, x.shape)
+    pw = None if weight is None else _mx_in(weight, "weight", _F32, dev, (H,))
+    packed, scale = _mx_out(M, H, x)
     r = None if delta is None else torch.empty_like(x)
     _check(lib.ar_rmsnorm_mxfp4(px, pd, AR_BF16 if delta is None else _dtype_code(delta), delta_scale, pw, M, H, eps,
                                 None if r is None else r.data_ptr(), packed.data_ptr(), scale.data_ptr(), _stream()))
@@ -347,20 +360,21 @@ def swiglu_mxfp4(gate: torch.Tensor, up: torch.Tensor):
     """silu(gate) * up as packed MXFP4 (packed, scale); gate and up bf16
     [M, F] with contiguous rows, which may be the halves of one [M, 2F]
     product (row strides multiples of 8)."""
-    pg = _mx_in(gate, "gate", _BF16, strided=True)
-    pu = _mx_in(up, "up", _BF16, gate.shape, strided=True)
+    dev = _mx_dev()
+    pg = _mx_in(gate, "gate", _BF16, dev, strided=True)
+    pu = _mx_in(up, "up", _BF16, dev, gate.shape, True)
     M, F = gate.shape
-    packed, scale = _mx_out(M, F, gate.device)
+    packed, scale = _mx_out(M, F, gate)
     # the stride of a lone row means nothing
     lg, lu = (gate.stride(0), up.stride(0)) if M > 1 else (F, F)
     _check(lib.ar_swiglu_mxfp4(pg, lg, pu, lu, M, F, packed.data_ptr(), scale.data_ptr(), _stream()))
     return packed, scale
 
 
-def _mx_y(out, out_dtype, M, N, dev):
+def _mx_y(out, out_dtype, M, N, like, dev):
     if out is None:
-        return torch.empty((M, N), dtype=out_dtype, device=dev)
-    _mx_in(out, "out", (out_dtype,), (M, N))
+        return like.new_empty((M, N), dtype=out_dtype)
+    _mx_in(out, "out", (out_dtype,), dev, (M, N))
     return out
 
 
@@ -369,13 +383,14 @@ def mxfp4_gemm(X: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, out_d
     """Y = X W^T with W the values of pack_mxfp4's output; X bf16 [M, K],
     packed uint8 [N, K/2], scale uint8 [N, K/32] -> Y [M, N] (fp32 sums, or
     their bf16 rounding)."""
-    px = _mx_in(X, "X", _BF16)
-    pp = _mx_in(packed, "packed", _U8)
+    dev = _mx_dev()
+    px = _mx_in(X, "X", _BF16, dev)
+    pp = _mx_in(packed, "packed", _U8, dev)
     (M, K), N = X.shape, packed.shape[0]
     if 2 * packed.shape[1] != K:
         raise ValueError(f"X has {K} columns, packed holds {2 * packed.shape[1]}")
-    ps = _mx_in(scale, "scale", _U8, (N, K // 32))
-    out = _mx_y(out, out_dtype, M, N, X.device)
+    ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
+    out = _mx_y(out, out_dtype, M, N, X, dev)
     _check(lib.ar_mxfp4_gemm(px, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _stream()))
     return out
 
@@ -384,14 +399,15 @@ def mxfp4_gemm_a4(x_packed: torch.Tensor, x_scale: torch.Tensor, packed: torch.T
                   out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
     """mxfp4_gemm with activations in packed MXFP4 too (x_packed uint8
     [M, K/2], x_scale uint8 [M, K/32], as the quantizing calls return them)."""
-    px = _mx_in(x_packed, "x_packed", _U8)
-    pp = _mx_in(packed, "packed", _U8)
+    dev = _mx_dev()
+    px = _mx_in(x_packed, "x_packed", _U8, dev)
+    pp = _mx_in(packed, "packed", _U8, dev)
     M, K, N = x_packed.shape[0], 2 * x_packed.shape[1], packed.shape[0]
     if 2 * packed.shape[1] != K:
         raise ValueError(f"x_packed holds {K} columns, packed {2 * packed.shape[1]}")
-    pxs = _mx_in(x_scale, "x_scale", _U8, (M, K // 32))
-    ps = _mx_in(scale, "scale", _U8, (N, K // 32))
-    out = _mx_y(out, out_dtype, M, N, x_packed.device)
+    pxs = _mx_in(x_scale, "x_scale", _U8, dev, (M, K // 32))
+    ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
+    out = _mx_y(out, out_dtype, M, N, x_packed, dev)
     _check(lib.ar_mxfp4_gemm_a4(px, pxs, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _stream()))
     return out
 
