@@ -235,14 +235,13 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[TM][TN], const Mx
 // banks.
 template <int BM, int BN, int NW>
 struct ScaleMover {
-    static constexpr int ROWS = BM + BN, QR = ROWS / 4, T = QR / (8 * NW);   // 8 rows per instruction
-    static_assert(BM == BN && T * 8 * NW == QR, "quarters must be of one operand and split over the wavefronts");
+    // eight rows per instruction; with an uneven split some are moved twice, to the same place
+    static constexpr int ROWS = BM + BN, QI = ROWS / 32, T = (QI + NW - 1) / NW;
+    static_assert(QI * 32 == ROWS && BM % 32 == 0, "a quarter is whole instructions, each of one operand");
     __amdgpu_buffer_rsrc_t rx, rw;
-    uint32_t off[T];
     uint32_t nb;
     int wave;
     __device__ __forceinline__ void init(const uint8_t* xs, int64_t xrows, const uint8_t* ws, int64_t wrows, int n, int w) {
-        const int lane = threadIdx.x & 63;
         wave = w;
         nb = (uint32_t)n;
         auto rsrc = [&](const uint8_t* p, int64_t rows) {
@@ -252,20 +251,19 @@ struct ScaleMover {
         };
         rx = rsrc(xs, xrows);
         rw = rsrc(ws, wrows);
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const int r = (t * NW + w) * 8 + lane / 8;   // a row of the quarter; r / 8 % 4 as in the whole
-            off[t] = (uint32_t)r * nb + (uint32_t)(((((lane % 8) >> 1) ^ ((r / 8) & 3)) << 3) + (lane & 1) * 4);
-        }
     }
     // quarter q of group g
     __device__ __forceinline__ void issue(char* lds, int g, int q) {
-        const uint32_t o = (uint32_t)(q & 1) * QR * nb + (uint32_t)g * 32u;
-        char* at = lds + (g & 1) * ROWS * 32 + q * QR * 32;
+        const uint32_t lane = threadIdx.x & 63;
+        char* at = lds + (g & 1) * ROWS * 32;
 #pragma unroll
-        for (int t = 0; t < T; ++t)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? rx : rw, (lds_void*)(at + (t * NW + wave) * 256), 4,
-                                                     (int)(off[t] + o), 0, 0, 0);
+        for (int t = 0; t < T; ++t) {
+            const int i = q * QI + (t * NW + wave) % QI, row = i * 8;   // rows row .. row + 7, X's first
+            const bool x = row < BM;
+            const uint32_t o = ((uint32_t)(x ? row : row - BM) + lane / 8) * nb + (uint32_t)g * 32u +
+                               ((((lane % 8) >> 1) ^ (uint32_t)(i & 3)) << 3) + (lane & 1) * 4;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(x ? rx : rw, (lds_void*)(at + i * 256), 4, (int)o, 0, 0, 0);
+        }
     }
 };
 
@@ -709,15 +707,16 @@ void launch_skinny(const MxGemmArgs& a, hipStream_t stream) {
 
 int64_t tiles(const MxGemmArgs& a, int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); }
 
+template <int BM, int BN>
 void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)tiles(a, 256, 256)), block(512);
+    const dim3 grid((unsigned)tiles(a, BM, BN)), block(512);
     const bool grouped = a.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
     if (a.y_bf16) {
-        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, true, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, true, false>), grid, block, 0, stream, a);
+        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, true, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, true, false>), grid, block, 0, stream, a);
     } else {
-        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, false, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<256, 256, 2, 4, false, false>), grid, block, 0, stream, a);
+        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, false, true>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, false, false>), grid, block, 0, stream, a);
     }
 }
 
@@ -731,7 +730,8 @@ void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
 //   16 x 28672 x 8192:  32x128 36, 32x64 39, 64x128 41 | 32x64 27, 32x32 31, 32x128 32
 //   64 x 4096 x 4096:   32x64 10, 64x64 13 | 32x32 6.0, 32x64 7.4
 //   130 x 4096 x 11008: 64x64 29, 32x64 33, 64x128 39 | 64x64 16, 32x64 20, 64x128 21
-//   512 x 11008 x 4096: 128x256 56, 64x128 58 | 256x256 28, 128x128 31, 64x128 33
+//   512 x 11008 x 4096: 128x256 56, 64x128 58 | 128x256 22, 256x256 29, 128x128 31
+//   1024 x 11008 x 4096 (packed): 256x256 33, 128x256 43
 // Up to 16 rows on up to 4096 outputs (one workgroup of 16 a CU) take the
 // skinny kernel, which has no ring to fill: 1 x 4096 x 11008 9.4 against 24 |
 // 7.9 against 11.
@@ -753,7 +753,8 @@ hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
     else if (tiles(a, 64, 128) <= 256) launch_ring<true, 64, 128, 1, 2, 2, 8>(a, stream);
     else if (tiles(a, 128, 128) <= 256 || a.K < 256 || a.N >= kMxTileMaxN)
         launch_ring<true, 128, 128, 2, 2, 2, 8>(a, stream);
-    else launch_a4_tile(a, stream);
+    else if (tiles(a, 128, 256) <= 256) launch_a4_tile<128, 256>(a, stream);
+    else launch_a4_tile<256, 256>(a, stream);
     return hipGetLastError();
 }
 
