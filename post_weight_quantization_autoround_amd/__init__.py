@@ -172,13 +172,7 @@ def _opt(t, name, dtype, shape):
     return None if t is None else _dev(t, name, dtype, shape)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream() -> int:
-    # the handle of torch.cuda.current_stream(), whose Stream object costs most of 3 us a call
-    if _raw_stream is not None and torch.cuda.is_initialized():
-        return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -296,7 +290,14 @@ def _mx_in(t, name, dtypes, dev, shape=None, strided=False):
 
 
 def _mx_dev():
+    # a tensor on a device exists, or every check below fails
     return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+# Handle of torch.cuda.current_stream(dev): building that Stream object takes
+# most of 3 us, a third of a small call.
+_mx_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 _F32_BF16 = (torch.float32, torch.bfloat16)
@@ -323,7 +324,7 @@ def pack_mxfp4(W: torch.Tensor, alpha: torch.Tensor | None = None):
     N, K = W.shape
     packed, scale = _mx_out(N, K, W)
     pa = None if alpha is None else _mx_in(alpha, "alpha", _F32, dev, scale.shape)
-    _check(lib.ar_pack_mxfp4(pw, _dtype_code(W), N, K, pa, packed.data_ptr(), scale.data_ptr(), _stream()))
+    _check(lib.ar_pack_mxfp4(pw, _dtype_code(W), N, K, pa, packed.data_ptr(), scale.data_ptr(), _mx_stream(dev)))
     return packed, scale
 
 
@@ -334,7 +335,7 @@ def unpack_mxfp4(packed: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dty
     N, K = packed.shape[0], 2 * packed.shape[1]
     ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
     out = packed.new_empty((N, K), dtype=out_dtype)
-    _check(lib.ar_unpack_mxfp4(pp, ps, N, K, out.data_ptr(), _dtype_code(out), _stream()))
+    _check(lib.ar_unpack_mxfp4(pp, ps, N, K, out.data_ptr(), _dtype_code(out), _mx_stream(dev)))
     return out
 
 
@@ -352,7 +353,7 @@ def rmsnorm_mxfp4(x: torch.Tensor, weight: torch.Tensor | None = None, eps: floa
     packed, scale = _mx_out(M, H, x)
     r = None if delta is None else torch.empty_like(x)
     _check(lib.ar_rmsnorm_mxfp4(px, pd, AR_BF16 if delta is None else _dtype_code(delta), delta_scale, pw, M, H, eps,
-                                None if r is None else r.data_ptr(), packed.data_ptr(), scale.data_ptr(), _stream()))
+                                None if r is None else r.data_ptr(), packed.data_ptr(), scale.data_ptr(), _mx_stream(dev)))
     return packed, scale, r
 
 
@@ -367,7 +368,7 @@ def swiglu_mxfp4(gate: torch.Tensor, up: torch.Tensor):
     packed, scale = _mx_out(M, F, gate)
     # the stride of a lone row means nothing
     lg, lu = (gate.stride(0), up.stride(0)) if M > 1 else (F, F)
-    _check(lib.ar_swiglu_mxfp4(pg, lg, pu, lu, M, F, packed.data_ptr(), scale.data_ptr(), _stream()))
+    _check(lib.ar_swiglu_mxfp4(pg, lg, pu, lu, M, F, packed.data_ptr(), scale.data_ptr(), _mx_stream(dev)))
     return packed, scale
 
 
@@ -391,7 +392,7 @@ def mxfp4_gemm(X: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, out_d
         raise ValueError(f"X has {K} columns, packed holds {2 * packed.shape[1]}")
     ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
     out = _mx_y(out, out_dtype, M, N, X, dev)
-    _check(lib.ar_mxfp4_gemm(px, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _stream()))
+    _check(lib.ar_mxfp4_gemm(px, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _mx_stream(dev)))
     return out
 
 
@@ -408,7 +409,7 @@ def mxfp4_gemm_a4(x_packed: torch.Tensor, x_scale: torch.Tensor, packed: torch.T
     pxs = _mx_in(x_scale, "x_scale", _U8, dev, (M, K // 32))
     ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
     out = _mx_y(out, out_dtype, M, N, x_packed, dev)
-    _check(lib.ar_mxfp4_gemm_a4(px, pxs, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _stream()))
+    _check(lib.ar_mxfp4_gemm_a4(px, pxs, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _mx_stream(dev)))
     return out
 
 
