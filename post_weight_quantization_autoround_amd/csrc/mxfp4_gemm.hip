@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(1024) mx_gemm_skinny_kernel(MxGemmArgs a) {
     store_y<BF16>(a.y, i * a.N + n0 + j, sum);
 }
 
-// ------------------------------------------------------ many rows of X ----
+// ----------------------------------------- many rows of packed operands ----
 // BM x BN outputs per workgroup, NWM x NWN wavefronts in 32 x 32 MFMA blocks.
 // A stage holds KS bytes of each operand row in LDS, moved there by
 // global_load_lds_dwordx4 (64 lanes x 16 bytes per instruction), two stages:
@@ -417,14 +417,18 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmA
     store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
 }
 
-// --------------------------------------------------- a few hundred rows ----
-// Tiles too small for a wavefront to own a full K: NWM x NWN wavefronts cover
-// BM x BN outputs and NWK such sets split every stage between them; their sums
-// meet in LDS at the end, in order.  A ring of four stages in LDS keeps three
-// in flight.  A stage is SB blocks: 256 k of packed operands, or 128 k where X
-// is bf16 (256 bytes of a row, as two 128-byte rows in LDS, one per 64 k).
-// The stage's 64-k steps go to the NWK sets in runs.  In the last stage lanes
-// past K load from past the buffers, which gives zeros.
+// -------------------------------------------------------------- the ring ----
+// NWM x NWN wavefronts cover BM x BN outputs in 32 x 32 MFMA blocks.  Where the
+// tile is too small for a wavefront to own a full K, NWK such sets split every
+// stage between them; their sums meet in LDS at the end, in order.  A ring of
+// NST stages in LDS keeps NST - 1 in flight, and one barrier a stage tells that
+// the next has landed and the one before is read.  A stage is SB blocks of a
+// row: SB * 16 bytes packed; bf16 X takes SB * 64, as SB / 2 rows of 128 bytes in
+// LDS, one per 64 k.  The stage's 64-k steps go to the NWK sets in runs.  In
+// the last stage lanes past K load from past the buffers, which gives zeros.
+// A tile column starts its K loop at a group of its own and wraps around, so
+// that the columns do not all stream the same part of their rows at a time (64
+// x 28672 x 8192, packed X: 31 against 34 us).
 template <int ROWS, int RB, int SUB, int NW>
 struct RingMover {
     // LDS row s * ROWS + r holds bytes [RB s, RB s + RB) of row r's stage
@@ -460,15 +464,16 @@ struct RingMover {
     }
 };
 
-// Scale bytes of ROWS rows in groups of four stages, 4 SB bytes a row: per-stage
-// reads straight from memory would take a cache line per row and stage and
-// cost more than the codes (64 x 64 tiles: 0.56 against 0.xx us a stage).
+// Scale bytes of ROWS rows in groups of one turn of the ring, GB bytes a row:
+// per-stage reads straight from memory would take a cache line per row and
+// stage and cost more than the codes (64 x 64 tiles of packed operands: 0.56
+// against 0.24 us a stage).
 // Rows start at any byte, so one dword more, from the aligned one before, is
-// moved (DW in all, RPI rows per instruction); the odd row pitch in LDS spreads
+// moved (DW dwords in all, RPI rows per instruction); the odd row pitch in LDS spreads
 // a read's rows over the banks.
-template <int ROWS, int SB, int NW>
+template <int ROWS, int GB, int NW>
 struct ScaleRing {
-    static constexpr int DW = SB + 1, RPI = 64 / DW;
+    static constexpr int DW = (GB + 6) / 4, RPI = 64 / DW;
     static constexpr int S = (ROWS + RPI * NW - 1) / (RPI * NW), BYTES = S * NW * 256;   // instructions per wavefront, buffer
     __amdgpu_buffer_rsrc_t rsrc;
     uint32_t off[S];
@@ -492,7 +497,7 @@ struct ScaleRing {
 #pragma unroll
         for (int t = 0; t < S; ++t)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (t * NW + wave) * 256), 4,
-                                                     (int)(off[t] + (uint32_t)(g * 4 * SB)), 0, 0, 0);
+                                                     (int)(off[t] + (uint32_t)(g * GB)), 0, 0, 0);
     }
     // where row r's bytes start in a buffer
     __device__ __forceinline__ int at(int r, int nb) const {
@@ -500,16 +505,16 @@ struct ScaleRing {
     }
 };
 
-template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB, bool BF16>
-__global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGemmArgs a) {
+template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB, int NST, int MINW, bool BF16>
+__global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kernel(MxGemmArgs a) {
     constexpr int NW = NWM * NWN * NWK, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32;
-    constexpr int NST = 4, XSUB = A4 ? 1 : SB / 2, STEPS = SB / 2, SPW = STEPS / NWK;
+    constexpr int XSUB = A4 ? 1 : SB / 2, STEPS = SB / 2, SPW = STEPS / NWK;
     constexpr int WB = SB * 16, XB = XSUB * BM * 128;
     constexpr int RED = NW * 16 * 36 * 4;   // half a block of every wavefront
     constexpr int STAGE = XB + BN * WB > RED ? XB + BN * WB : RED;
-    using SX = ScaleRing<BM, SB, NW>;
-    using SW = ScaleRing<BN, SB, NW>;
-    __shared__ __attribute__((aligned(1024))) char st0[STAGE], st1[STAGE], st2[STAGE], st3[STAGE];
+    using SX = ScaleRing<BM, SB * NST, NW>;
+    using SW = ScaleRing<BN, SB * NST, NW>;
+    __shared__ __attribute__((aligned(1024))) char st0[STAGE], st1[STAGE], st2[STAGE], st3[NST > 3 ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) char ssw[2 * SW::BYTES], ssx[A4 ? 2 * SX::BYTES : 16];
     static_assert(SPW * NWK == STEPS, "the steps of a stage split over the sets");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
 
     constexpr int LPW = decltype(mx)::Q + decltype(mw)::Q;   // loads per wavefront and stage
     constexpr int SPG = SW::S + (A4 ? SX::S : 0);            // and more in a group's first stage
-    const int rot = nk % 4 == 0 ? (int)(tile_n % (uint32_t)(nk / 4)) * 4 : 0;
+    const int rot = nk % NST == 0 ? (int)(tile_n % (uint32_t)(nk / NST)) * NST : 0;
     auto turned = [&](int kt) { const int k = kt + rot; return k < nk ? k : k - nk; };
     auto issue = [&](int kt, char* st) __attribute__((always_inline)) {
         const int kk = turned(kt), left = kt < nk ? nb - kk * SB : 0;   // stages past the last load nothing, but keep the count
@@ -544,16 +549,16 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
         mw.issue(st + XB, kk, left * 16);
     };
     auto issue_scales = [&](int g) __attribute__((always_inline)) {
-        const int gg = turned(4 * g) >> 2;
+        const int gg = turned(NST * g) / NST;
         sw.issue(ssw + (g & 1) * SW::BYTES, gg);
         if constexpr (A4) sx.issue(ssx + (g & 1) * SX::BYTES, gg);
     };
     // A group's scales in registers, read from LDS at its start: later, the
     // next group's may be on their way into the other buffer.
-    uint32_t cx[4][SPW][TM], cw[4][SPW][TN];
+    uint32_t cx[NST][SPW][TM], cw[NST][SPW][TN];
     auto read_scales = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
+        for (int p = 0; p < NST; ++p)
 #pragma unroll
             for (int t = 0; t < SPW; ++t) {
 #pragma unroll
@@ -632,12 +637,12 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
         gemm::static_for<NST>([&](auto S) {
             constexpr int p = decltype(S)::value;
             using Prev = std::integral_constant<int, (p + NST - 1) % NST>;
-            arrive(std::integral_constant<int, (NST - 2) * LPW + (p == 1 || p == 2 ? SPG : 0)>{});
+            arrive(std::integral_constant<int, (NST - 2) * LPW + (p >= 1 && p <= NST - 2 ? SPG : 0)>{});
             if constexpr (p == 0) {
-                read_scales(kt >> 2);
+                read_scales(kt / NST);
                 read_unit(buf(S), U0{});
                 __builtin_amdgcn_sched_barrier(0);
-                issue_scales((kt >> 2) + 1);
+                issue_scales((kt / NST) + 1);
             } else {
                 read_unit(buf(S), U0{});
                 __builtin_amdgcn_sched_barrier(0);
@@ -649,7 +654,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
         constexpr int p = decltype(S)::value;
         if (kt + p < nk) {
             arrive(std::integral_constant<int, (NST - 2 - p) * LPW>{});
-            if constexpr (p == 0) read_scales(kt >> 2);
+            if constexpr (p == 0) read_scales(kt / NST);
             read_unit(buf(S), U0{});
             compute(kt + p, buf(S), S);
         }
@@ -691,11 +696,11 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64) mx_gemm_ring_kernel(MxGe
     });
 }
 
-template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB>
+template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB, int NST, int MINW = 1>
 void launch_ring(const MxGemmArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN))), block(NWM * NWN * NWK * 64);
-    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, SB, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, SB, false>), grid, block, 0, stream, a);
+    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, SB, NST, MINW, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((mx_gemm_ring_kernel<A4, BM, BN, NWM, NWN, NWK, SB, NST, MINW, false>), grid, block, 0, stream, a);
 }
 
 template <bool A4>
@@ -726,33 +731,45 @@ void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
 // CUs, otherwise the largest: a workgroup's time is that of its K loop, most of
 // it latency, so one round of small tiles beats a part-filled round of large
 // ones, and with several rounds what counts is how often a tile re-reads its
-// operands.  Measured (us, bf16 X | packed X; smaller and larger neighbour):
-//   16 x 28672 x 8192:  32x128 36, 32x64 39, 64x128 41 | 32x64 27, 32x32 31, 32x128 32
-//   64 x 4096 x 4096:   32x64 10, 64x64 13 | 32x32 6.0, 32x64 7.4
-//   130 x 4096 x 11008: 64x64 29, 32x64 33, 64x128 39 | 64x64 16, 32x64 20, 64x128 21
-//   512 x 11008 x 4096: 128x256 56, 64x128 58 | 128x256 22, 256x256 29, 128x128 31
-//   1024 x 11008 x 4096 (packed): 256x256 33, 128x256 43
+// operands.  Measured (us, the choice first):
+//   bf16 X: 16 x 28672 x 8192 32x128 29, 32x64 34, 64x128 39; 64 x 4096 x 4096
+//   32x64 10, 64x64 14; 130 x 4096 x 11008 64x64 30, 64x128 39; 256 x 11008 x
+//   4096 64x128 in two rounds 36, 64x64 41, 128x256 54; 512 x 11008 x 4096
+//   128x256 55, 64x128 58; 2048 x 11008 x 4096 128x256 168, 256x256 182; 8192 x
+//   8192 x 8192 256x256 780 (1.41 PFLOP/s), 128x256 831
+//   packed X: 16 x 28672 x 8192 32x64 27, 32x32 31, 32x128 32; 64 x 4096 x 4096
+//   32x32 6.0, 32x64 7.4; 130 x 4096 x 11008 64x64 16, 32x64 20, 64x128 21; 256 x
+//   11008 x 4096 128x128 17, 128x256 20; 512 x 11008 x 4096 128x256 22, 256x256
+//   29, 128x128 31; 1024 x 11008 x 4096 256x256 33, 128x256 43
 // Up to 16 rows on up to 4096 outputs (one workgroup of 16 a CU) take the
-// skinny kernel, which has no ring to fill: 1 x 4096 x 11008 9.4 against 24 |
-// 7.9 against 11.
+// skinny kernel, which has no ring to fill: 1 x 4096 x 11008 9.4 against 24
+// (bf16), 7.9 against 11 (packed).
 hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
     if (a.M <= 16 && a.N <= 4096) launch_skinny<false>(a, stream);
-    else if (tiles(a, 32, 64) <= 256) launch_ring<false, 32, 64, 1, 2, 2, 4>(a, stream);
-    else if (a.M <= 32) launch_ring<false, 32, 128, 1, 2, 2, 4>(a, stream);
-    else if (tiles(a, 64, 64) <= 256) launch_ring<false, 64, 64, 1, 2, 2, 4>(a, stream);
-    else if (tiles(a, 64, 128) <= 256) launch_ring<false, 64, 128, 2, 2, 2, 4>(a, stream);
-    else launch_ring<false, 128, 256, 2, 4, 1, 2>(a, stream);
+    else if (tiles(a, 32, 64) <= 256) launch_ring<false, 32, 64, 1, 2, 2, 8, 3>(a, stream);
+    else if (a.M <= 32) launch_ring<false, 32, 128, 1, 2, 2, 8, 4>(a, stream);
+    else if (tiles(a, 64, 64) <= 256) launch_ring<false, 64, 64, 1, 1, 4, 8, 3>(a, stream);
+    else if (tiles(a, 64, 128) <= 512) launch_ring<false, 64, 128, 2, 2, 2, 8, 3>(a, stream);
+    else if (tiles(a, 128, 256) <= 256) launch_ring<false, 128, 256, 2, 4, 1, 4, 3>(a, stream);
+    else {
+        // Several rounds: 256x256 is 6% faster a flop, 128x256 (two workgroups a
+        // CU, so at most 128 registers) fills its last round better.
+        const int64_t big = tiles(a, 256, 256), small = tiles(a, 128, 256);
+        const double full_big = (double)big / (double)((big + 255) / 256), full_small = (double)small / (double)((small + 255) / 256);
+        if (1.06 * full_big >= full_small) launch_ring<false, 256, 256, 2, 4, 1, 2, 3>(a, stream);
+        else launch_ring<false, 128, 256, 2, 4, 1, 2, 3, 4>(a, stream);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
     if (a.M <= 16 && a.N <= 4096) launch_skinny<true>(a, stream);
-    else if (tiles(a, 32, 32) <= 256) launch_ring<true, 32, 32, 1, 1, 4, 8>(a, stream);
-    else if (tiles(a, 32, 64) <= 256 || a.M <= 32) launch_ring<true, 32, 64, 1, 1, 4, 8>(a, stream);
-    else if (tiles(a, 64, 64) <= 256) launch_ring<true, 64, 64, 1, 1, 4, 8>(a, stream);
-    else if (tiles(a, 64, 128) <= 256) launch_ring<true, 64, 128, 1, 2, 2, 8>(a, stream);
+    else if (tiles(a, 32, 32) <= 256) launch_ring<true, 32, 32, 1, 1, 4, 8, 4>(a, stream);
+    else if (tiles(a, 32, 64) <= 256 || a.M <= 32) launch_ring<true, 32, 64, 1, 1, 4, 8, 4>(a, stream);
+    else if (tiles(a, 64, 64) <= 256) launch_ring<true, 64, 64, 1, 1, 4, 8, 4>(a, stream);
+    else if (tiles(a, 64, 128) <= 256) launch_ring<true, 64, 128, 1, 2, 2, 8, 4>(a, stream);
     else if (tiles(a, 128, 128) <= 256 || a.K < 256 || a.N >= kMxTileMaxN)
-        launch_ring<true, 128, 128, 2, 2, 2, 8>(a, stream);
+        launch_ring<true, 128, 128, 2, 2, 2, 8, 4>(a, stream);
     else if (tiles(a, 128, 256) <= 256) launch_a4_tile<128, 256>(a, stream);
     else launch_a4_tile<256, 256>(a, stream);
     return hipGetLastError();
