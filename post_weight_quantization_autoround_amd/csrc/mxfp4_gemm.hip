@@ -476,8 +476,8 @@ struct ScaleRing {
     static constexpr int DW = (GB + 6) / 4, RPI = 64 / DW;
     static constexpr int S = (ROWS + RPI * NW - 1) / (RPI * NW), BYTES = S * NW * 256;   // instructions per wavefront, buffer
     __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t off[S];
-    int wave, shift;   // shift: the base pointer's bytes past a dword boundary
+    uint32_t first[S];   // this lane's row's first byte
+    int wave, shift;     // shift: the base pointer's bytes past a dword boundary
     __device__ __forceinline__ void init(const uint8_t* base, int64_t rows, int nb, int w) {
         const int lane = threadIdx.x & 63;
         wave = w;
@@ -488,21 +488,21 @@ struct ScaleRing {
 #pragma unroll
         for (int t = 0; t < S; ++t) {
             const int r = (t * NW + w) * RPI + lane / DW;
-            off[t] = lane < RPI * DW && r < ROWS
-                         ? (((uint32_t)r * (uint32_t)nb + (uint32_t)shift) & ~3u) + (uint32_t)(lane % DW) * 4u
-                         : 0x80000000u;
+            first[t] = lane < RPI * DW && r < ROWS ? (uint32_t)r * (uint32_t)nb + (uint32_t)shift : 0x80000000u;
         }
     }
     __device__ __forceinline__ void issue(char* lds, int g) {
 #pragma unroll
         for (int t = 0; t < S; ++t)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (t * NW + wave) * 256), 4,
-                                                     (int)(off[t] + (uint32_t)(g * GB)), 0, 0, 0);
+                                                     (int)(((first[t] + (uint32_t)(g * GB)) & ~3u) +
+                                                           (threadIdx.x & 63) % DW * 4u), 0, 0, 0);
     }
-    // where row r's bytes start in a buffer
-    __device__ __forceinline__ int at(int r, int nb) const {
-        return r / RPI * 256 + r % RPI * (4 * DW) + (((int)((uint32_t)r * (uint32_t)nb) + shift) & 3);
-    }
+    // where row r's dwords start in a buffer, and the row's first byte
+    __device__ __forceinline__ int at(int r) const { return r / RPI * 256 + r % RPI * (4 * DW); }
+    __device__ __forceinline__ int byte(int r, int nb) const { return (int)((uint32_t)r * (uint32_t)nb) + shift; }
+    // group g's first byte within those dwords
+    static __device__ __forceinline__ int skip(int byte, int g) { return (GB % 4 == 0 ? byte : byte + g * GB) & 3; }
 };
 
 template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB, int NST, int MINW, bool BF16>
@@ -533,11 +533,17 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     SW sw;
     if constexpr (A4) sx.init(a.xs + m0 * nb, a.M - m0, nb, wave);
     sw.init(a.ws + n0 * nb, a.N - n0, nb, wave);
-    int xo[TM], wo[TN];   // this lane's first scale byte of a group, per row block
+    int xo[TM], wo[TN], xb[TM], wb[TN];   // this lane's rows of scales: place in a buffer, first byte
 #pragma unroll
-    for (int i = 0; i < TM; ++i) xo[i] = A4 ? sx.at(wm * WM + i * 32 + r, nb) + 2 * wk * SPW + half : 0;
+    for (int i = 0; i < TM; ++i) {
+        xo[i] = A4 ? sx.at(wm * WM + i * 32 + r) + 2 * wk * SPW + half : 0;
+        xb[i] = A4 ? sx.byte(wm * WM + i * 32 + r, nb) : 0;
+    }
 #pragma unroll
-    for (int i = 0; i < TN; ++i) wo[i] = sw.at(wn * WN + i * 32 + r, nb) + 2 * wk * SPW + half;
+    for (int i = 0; i < TN; ++i) {
+        wo[i] = sw.at(wn * WN + i * 32 + r) + 2 * wk * SPW + half;
+        wb[i] = sw.byte(wn * WN + i * 32 + r, nb);
+    }
 
     constexpr int LPW = decltype(mx)::Q + decltype(mw)::Q;   // loads per wavefront and stage
     constexpr int SPG = SW::S + (A4 ? SX::S : 0);            // and more in a group's first stage
@@ -557,17 +563,23 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     // next group's may be on their way into the other buffer.
     uint32_t cx[NST][SPW][TM], cw[NST][SPW][TN];
     auto read_scales = [&](int g) __attribute__((always_inline)) {
+        const int gg = turned(NST * g) / NST;
 #pragma unroll
-        for (int p = 0; p < NST; ++p)
+        for (int i = 0; i < TN; ++i) {
+            const char* at = ssw + (g & 1) * SW::BYTES + wo[i] + SW::skip(wb[i], gg);
 #pragma unroll
-            for (int t = 0; t < SPW; ++t) {
+            for (int p = 0; p < NST; ++p)
 #pragma unroll
-                for (int i = 0; i < TN; ++i)
-                    cw[p][t][i] = *reinterpret_cast<const uint8_t*>(ssw + (g & 1) * SW::BYTES + wo[i] + SB * p + 2 * t);
-                if constexpr (A4)
+                for (int t = 0; t < SPW; ++t) cw[p][t][i] = *reinterpret_cast<const uint8_t*>(at + SB * p + 2 * t);
+        }
+        if constexpr (A4)
 #pragma unroll
-                    for (int i = 0; i < TM; ++i)
-                        cx[p][t][i] = *reinterpret_cast<const uint8_t*>(ssx + (g & 1) * SX::BYTES + xo[i] + SB * p + 2 * t);
+            for (int i = 0; i < TM; ++i) {
+                const char* at = ssx + (g & 1) * SX::BYTES + xo[i] + SX::skip(xb[i], gg);
+#pragma unroll
+                for (int p = 0; p < NST; ++p)
+#pragma unroll
+                    for (int t = 0; t < SPW; ++t) cx[p][t][i] = *reinterpret_cast<const uint8_t*>(at + SB * p + 2 * t);
             }
     };
     f32x16 acc[TM][TN] = {};

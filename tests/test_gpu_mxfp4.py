@@ -225,6 +225,67 @@ def test_products_exact(ar, m, n, k):
         np.testing.assert_array_equal(_np(ar.mxfp4_gemm_a4(_dev(xp), _dev(xs), _dev(wp), _dev(ws), out_dtype=dt)), want)
 
 
+# Every tile the products choose from (the choice goes by how many tiles there are), with K that ends inside a stage and
+# K that does not, rows of scales on and off dword boundaries.
+TILED = [(17, 9000, 96), (17, 20000, 1056), (40, 5000, 288), (130, 4200, 416), (130, 4200, 1024), (130, 9000, 288),
+         (300, 9000, 160), (300, 9000, 640), (300, 17000, 288), (300, 17000, 384), (520, 17000, 288), (520, 17000, 768),
+         (520, 17000, 128), (600, 9000, 352), (1100, 8000, 96), (1100, 8000, 1088), (2000, 8300, 160), (2000, 8300, 512)]
+
+
+@pytest.mark.parametrize("m,n,k", TILED)
+def test_products_exact_over_the_tiles(ar, m, n, k):
+    rng = np.random.default_rng(m + 3 * n + 7 * k)
+    wp, ws = (_dev(t) for t in _exact_operand(rng, n, k))
+    xp, xs = (_dev(t) for t in _exact_operand(rng, m, k))
+    X, W = (_dev(mx.values(*(t.cpu().numpy() for t in p))) for p in ((xp, xs), (wp, ws)))
+    want = (X @ W.t()).float()                        # fp64 products and sums of these operands are exact
+    for dt in (torch.float32, torch.bfloat16):
+        print(f"a16 {m}x{n}x{k} {dt}", flush=True)
+        assert torch.equal(ar.mxfp4_gemm(X.bfloat16(), wp, ws, out_dtype=dt), want.to(dt))
+        print(f"a4 {m}x{n}x{k} {dt}", flush=True)
+        assert torch.equal(ar.mxfp4_gemm_a4(xp, xs, wp, ws, out_dtype=dt), want.to(dt))
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 40, 32), (16, 300, 288), (40, 5000, 160), (130, 4200, 288), (300, 9000, 96),
+                                   (300, 17000, 288), (520, 17000, 352), (1100, 8000, 96), (2000, 8300, 160)])
+def test_products_keep_rows_apart(ar, m, n, k):
+    # every second row of X and of W is NaN throughout: the others, whose last stage ends where such a row begins,
+    # are untouched
+    rng = np.random.default_rng(m + n + k)
+    wp, ws = (_dev(t) for t in _exact_operand(rng, n, k))
+    xp, xs = (_dev(t) for t in _exact_operand(rng, m, k))
+    X, W = (_dev(mx.values(*(t.cpu().numpy() for t in p))) for p in ((xp, xs), (wp, ws)))
+    want = (X @ W.t()).float()[::2, ::2]
+    ws[1::2] = 255
+    xs[1::2] = 255
+    x16 = X.bfloat16()
+    x16[1::2] = float("nan")
+    for Y in (ar.mxfp4_gemm(x16, wp, ws), ar.mxfp4_gemm_a4(xp, xs, wp, ws)):
+        assert torch.equal(Y[::2, ::2], want)
+        assert Y[1::2].isnan().all() and Y[:, 1::2].isnan().all()
+
+
+@pytest.mark.parametrize("m,n,k", [(2, 64, 256), (40, 5000, 256), (300, 17000, 256), (520, 17000, 512)])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_scales_at_any_address(ar, m, n, k, off):
+    rng = np.random.default_rng(off)
+    wp, ws = _exact_operand(rng, n, k)
+    xp, xs = _exact_operand(rng, m, k)
+
+    def moved(a):
+        buf = torch.full((a.size + 8,), 255, dtype=torch.uint8, device="cuda")
+        out = buf[off:off + a.size].view(a.shape)
+        out.copy_(_dev(a))
+        assert out.data_ptr() % 4 == off
+        return out
+
+    args = (_dev(wp), _dev(ws))
+    want = ar.mxfp4_gemm_a4(_dev(xp), _dev(xs), *args)
+    assert torch.equal(ar.mxfp4_gemm_a4(_dev(xp), moved(xs), args[0], moved(ws)), want)
+    x16 = ar.unpack_mxfp4(_dev(xp), moved(xs), out_dtype=torch.bfloat16)
+    assert torch.equal(ar.mxfp4_gemm(x16, args[0], moved(ws)), want)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 520, 4096), (16, 300, 11008), (40, 257, 2080), (130, 512, 4096),
                                    (520, 300, 1056)])
 def test_products_general(ar, m, n, k):
