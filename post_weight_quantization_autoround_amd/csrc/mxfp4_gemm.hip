@@ -187,13 +187,6 @@ struct Mover {
     }
 };
 
-// Row r's offset into a matrix of pitch `pitch`, relative to row0, clamped to
-// the last row.
-__device__ __forceinline__ uint32_t row_offset(int64_t row0, int r, int64_t rows, int64_t pitch) {
-    const int64_t last = rows - 1 - row0;
-    return (uint32_t)((r < last ? r : last) * pitch);
-}
-
 // Writes a wavefront's blocks of the tile at (m0, n0): element e of a block is
 // row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.  Buffer stores with
 // 32-bit offsets (kMxTileMaxN) from the tile's first row drop rows past M.
@@ -228,9 +221,9 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[TM][TN], const Mx
 // Scale bytes of the packed-activation tiles.  A row's scales of a stage are
 // eight bytes and rows lie K / 32 bytes apart, so fetching a stage at a time
 // takes a cache line per row and stage (100 of 575 us at 4096 x 28672 x 8192).
-// Where rows are dword-aligned (K a multiple of 128) they come in groups of
-// four stages instead, 32 bytes a row, moved to LDS a quarter of the rows per
-// stage: two groups of (BM + BN) * 32 bytes.  Row r's eight-byte piece p lies
+// They come in groups of four stages instead, 32 bytes a row, moved to LDS a
+// quarter of the rows per stage: two groups of (BM + BN) * 32 bytes.  Rows have
+// to start at a dword.  Row r's eight-byte piece p lies
 // at p ^ (r / 8 % 4), which spreads the 32 rows that a read takes over all
 // banks.
 template <int BM, int BN, int NW>
@@ -267,18 +260,17 @@ struct ScaleMover {
     }
 };
 
-// Both operands packed, K >= 256: a stage is 256 k (128 bytes a row), four
-// MFMA steps of 64 k.  A lane holds row l % 32 and blocks 2 s + l / 32, s =
+// Both operands packed, K a multiple of 128 and at least 256: a stage is 256 k
+// (128 bytes a row), four MFMA steps of 64 k.  A lane holds row l % 32 and blocks 2 s + l / 32, s =
 // 0..3, of the stage: one byte permute of the row's eight scale bytes leaves
 // its four in the order of the steps, where the MFMA's operand selects take
-// them.  GROUPED: scales by ScaleMover; otherwise straight from global memory
-// a stage ahead.  Blocks past K get scale byte 0 on both sides: their
-// products, at most 36 * 2^-254, are zeros in fp32.
-template <int BM, int BN, int NWM, int NWN, bool BF16, bool GROUPED>
+// them.  Blocks past K get scale byte 0 on both sides: their products, at most
+// 36 * 2^-254, are zeros in fp32.
+template <int BM, int BN, int NWM, int NWN, bool BF16>
 __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmArgs a) {
     constexpr int NW = NWM * NWN, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32, KS = 128;
     __shared__ __attribute__((aligned(1024))) char sx0[BM * KS], sw0[BN * KS], sx1[BM * KS], sw1[BN * KS];
-    __shared__ __attribute__((aligned(1024))) char ssc[GROUPED ? 2 * (BM + BN) * 32 : 16];
+    __shared__ __attribute__((aligned(1024))) char ssc[2 * (BM + BN) * 32];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / NWN, wn = wave % NWN, r = lane & 31, half = lane >> 5;
     uint32_t tile_m, tile_n;
@@ -292,38 +284,19 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmA
     mw.init(a.wp, n0, a.N, a.K >> 1, wave);
     const uint8_t *xs = a.xs + m0 * nb, *ws = a.ws + n0 * nb;
     const uint32_t sel = half ? 0x07050301u : 0x06040200u;
-    uint64_t nx[TM], nw[TN];
-    uint32_t xo[TM], wo[TN];
+    uint64_t nx[TM], nw[TN];   // a stage's scale bytes
     ScaleMover<BM, BN, NW> ms;
-    if constexpr (GROUPED) {
-        ms.init(xs, a.M - m0, ws, a.N - n0, nb, wave);
-    } else {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) xo[i] = row_offset(m0, wm * WM + i * 32 + r, a.M, nb);
-#pragma unroll
-        for (int i = 0; i < TN; ++i) wo[i] = row_offset(n0, wn * WN + i * 32 + r, a.N, nb);
-    }
-    // The scale bytes of stage kt.  Not GROUPED, the last, partial stage reads
-    // the row's last eight.
+    ms.init(xs, a.M - m0, ws, a.N - n0, nb, wave);
     auto load_scales = [&](int kt) __attribute__((always_inline)) {
-        if constexpr (GROUPED) {
-            const char* g = ssc + ((kt >> 2) & 1) * (BM + BN) * 32 + r * 32 + (((kt & 3) ^ ((r >> 3) & 3)) << 3);
+        const char* g = ssc + ((kt >> 2) & 1) * (BM + BN) * 32 + r * 32 + (((kt & 3) ^ ((r >> 3) & 3)) << 3);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) nx[i] = *reinterpret_cast<const uint64_t*>(g + (wm * WM + i * 32) * 32);
+        for (int i = 0; i < TM; ++i) nx[i] = *reinterpret_cast<const uint64_t*>(g + (wm * WM + i * 32) * 32);
 #pragma unroll
-            for (int i = 0; i < TN; ++i) nw[i] = *reinterpret_cast<const uint64_t*>(g + (BM + wn * WN + i * 32) * 32);
-        } else {
-            const int b = kt * 8 < nb - 8 ? kt * 8 : nb - 8;
-#pragma unroll
-            for (int i = 0; i < TM; ++i) __builtin_memcpy(&nx[i], xs + b + xo[i], 8);
-#pragma unroll
-            for (int i = 0; i < TN; ++i) __builtin_memcpy(&nw[i], ws + b + wo[i], 8);
-        }
+        for (int i = 0; i < TN; ++i) nw[i] = *reinterpret_cast<const uint64_t*>(g + (BM + wn * WN + i * 32) * 32);
     };
     auto use = [&](uint64_t v, int kt) __attribute__((always_inline)) {
         const int past = kt * 8 - (nb - 8);   // blocks of the stage past K
-        if constexpr (GROUPED) v &= ~0ull >> (past > 0 ? 8 * (past < 8 ? past : 7) : 0);
-        else v >>= past > 0 ? 8 * (past < 8 ? past : 7) : 0;
+        v &= ~0ull >> (past > 0 ? 8 * (past < 8 ? past : 7) : 0);
         return __builtin_amdgcn_perm((uint32_t)(v >> 32), (uint32_t)v, sel);
     };
 
@@ -346,19 +319,16 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmA
     };
     using I0 = std::integral_constant<int, 0>;
 
-    if constexpr (GROUPED)
-        for (int q = 0; q < 4; ++q) ms.issue(ssc, 0, q);
+    for (int q = 0; q < 4; ++q) ms.issue(ssc, 0, q);
     mx.issue(sx0, 0);
     mw.issue(sw0, 0);
-    if constexpr (!GROUPED) load_scales(0);
     wait_vmcnt<0>();
     lds_barrier();
-    if constexpr (GROUPED) load_scales(0);
+    load_scales(0);
     use_scales(0);
     mx.issue(sx1, nk > 1 ? 1 : 0);
     mw.issue(sw1, nk > 1 ? 1 : 0);
-    if constexpr (GROUPED) ms.issue(ssc, 1, 0);
-    else load_scales(nk > 1 ? 1 : 0);
+    ms.issue(ssc, 1, 0);
     gemm::static_for<TM + TN>([&](auto F) { frag(sx0, sw0, I0{}, F); });
 
     // Stage kt, its data in X, W: during step s the fragments of step s + 1 are
@@ -379,14 +349,9 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(MxGemmA
             constexpr int s = decltype(S)::value, n = TM * TN;
             if constexpr (s == 3) {
                 asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                if constexpr (GROUPED) {
-                    load_scales(kt + 1);
-                    use_scales(kt + 1);
-                    ms.issue(ssc, ((kt + 1) >> 2) + 1, (kt + 1) & 3);
-                } else {
-                    use_scales(kt + 1);
-                    load_scales(next);
-                }
+                load_scales(kt + 1);
+                use_scales(kt + 1);
+                ms.issue(ssc, ((kt + 1) >> 2) + 1, (kt + 1) & 3);
             }
             gemm::static_for<n>([&](auto Kk) {
                 constexpr int k = decltype(Kk)::value, i = k / TN, j = k % TN;
@@ -727,14 +692,8 @@ int64_t tiles(const MxGemmArgs& a, int64_t bm, int64_t bn) { return ((a.M + bm -
 template <int BM, int BN>
 void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
     const dim3 grid((unsigned)tiles(a, BM, BN)), block(512);
-    const bool grouped = a.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
-    if (a.y_bf16) {
-        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, true, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, true, false>), grid, block, 0, stream, a);
-    } else {
-        if (grouped) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, false, true>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, false, false>), grid, block, 0, stream, a);
-    }
+    if (a.y_bf16) hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((mx_gemm_a4_tile_kernel<BM, BN, 2, 4, false>), grid, block, 0, stream, a);
 }
 
 }  // namespace
@@ -775,12 +734,15 @@ hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
+    // what the tile kernels need; the ring takes any K and address
+    const bool aligned = a.K % 128 == 0 && a.K >= 256 &&
+                         ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
     if (a.M <= 16 && a.N <= 4096) launch_skinny<true>(a, stream);
     else if (tiles(a, 32, 32) <= 256) launch_ring<true, 32, 32, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 32, 64) <= 256 || a.M <= 32) launch_ring<true, 32, 64, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 64, 64) <= 256) launch_ring<true, 64, 64, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 64, 128) <= 256) launch_ring<true, 64, 128, 1, 2, 2, 8, 4>(a, stream);
-    else if (tiles(a, 128, 128) <= 256 || a.K < 256 || a.N >= kMxTileMaxN)
+    else if (tiles(a, 128, 128) <= 256 || !aligned || a.N >= kMxTileMaxN)
         launch_ring<true, 128, 128, 2, 2, 2, 8, 4>(a, stream);
     else if (tiles(a, 128, 256) <= 256) launch_a4_tile<128, 256>(a, stream);
     else launch_a4_tile<256, 256>(a, stream);
