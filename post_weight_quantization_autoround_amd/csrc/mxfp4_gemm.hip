@@ -474,7 +474,7 @@ template <bool A4, int BM, int BN, int NWM, int NWN, int NWK, int SB, int NST, i
 __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kernel(MxGemmArgs a) {
     constexpr int NW = NWM * NWN * NWK, WM = BM / NWM, WN = BN / NWN, TM = WM / 32, TN = WN / 32;
     constexpr int XSUB = A4 ? 1 : SB / 2, STEPS = SB / 2, SPW = STEPS / NWK;
-    constexpr int WB = SB * 16, XB = XSUB * BM * 128;
+    constexpr int WB = SB * 16, XR = A4 ? WB : 128, XB = XSUB * BM * XR;   // bytes of an LDS row of W, of X
     constexpr int RED = NW * 16 * 36 * 4;   // half a block of every wavefront
     constexpr int STAGE = XB + BN * WB > RED ? XB + BN * WB : RED;
     using SX = ScaleRing<BM, SB * NST, NW>;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
     const int nb = (int)(a.K >> 5), nk = (nb + SB - 1) / SB;
 
-    RingMover<BM, 128, XSUB, NW> mx;
+    RingMover<BM, XR, XSUB, NW> mx;
     RingMover<BN, WB, 1, NW> mw;
     if constexpr (A4) mx.init(a.xp, m0, a.M, a.K >> 1, wave);
     else mx.init(a.x, m0, a.M, 2 * a.K, wave);
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     constexpr int UNITS = A4 ? SPW : 4 * SPW;
     u32x4 xf[2][TM], wf[2][TN];   // bf16: wf holds a whole step's codes, in set step % 2
     // (opaque, so that the compiler keeps to one base and constant offsets, for which it can tell the buffers apart)
-    int xrow = (wm * WM + (A4 ? 0 : wk * SPW * BM)) * 128, wrow = wn * WN * WB;
+    int xrow = (wm * WM + (A4 ? 0 : wk * SPW * BM)) * XR, wrow = wn * WN * WB;
     asm volatile("" : "+v"(xrow), "+v"(wrow));
     auto read_unit = [&](const char* st, auto U) __attribute__((always_inline)) {
         constexpr int u = decltype(U)::value, t = A4 ? u : u / 4, q = u % 4;
@@ -564,9 +564,9 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
 #pragma unroll
             for (int j = 0; j < TN; ++j) wf[t & 1][j] = *reinterpret_cast<const u32x4*>(st + at + (XB + j * 32 * WB));
         }
-        const int at = A4 ? xrow + lds_at<128>(r, 2 * s + half) : xrow + lds_at<128>(r, 4 * half + q) + t * (BM * 128);
+        const int at = xrow + (A4 ? lds_at<XR>(r, 2 * s + half) : lds_at<XR>(r, 4 * half + q) + t * (BM * XR));
 #pragma unroll
-        for (int i = 0; i < TM; ++i) xf[u & 1][i] = *reinterpret_cast<const u32x4*>(st + at + i * 4096);
+        for (int i = 0; i < TM; ++i) xf[u & 1][i] = *reinterpret_cast<const u32x4*>(st + at + i * 32 * XR);
     };
     auto compute = [&](int kt, const char* st, auto Slot) __attribute__((always_inline)) {
         constexpr int p = decltype(Slot)::value;
@@ -734,16 +734,17 @@ hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
-    // what the tile kernels need; the ring takes any K and address
-    const bool aligned = a.K % 128 == 0 && a.K >= 256 &&
+    // What the tile kernels need; the ring takes any K and address (2048 x 11008 x
+    // 4128: 88 us in 256x256 tiles, 109 in 128x128; 512 rows: 39 and 31).
+    const bool aligned = a.K % 128 == 0 && a.K >= 256 && a.N < kMxTileMaxN &&
                          ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
     if (a.M <= 16 && a.N <= 4096) launch_skinny<true>(a, stream);
     else if (tiles(a, 32, 32) <= 256) launch_ring<true, 32, 32, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 32, 64) <= 256 || a.M <= 32) launch_ring<true, 32, 64, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 64, 64) <= 256) launch_ring<true, 64, 64, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 64, 128) <= 256) launch_ring<true, 64, 128, 1, 2, 2, 8, 4>(a, stream);
-    else if (tiles(a, 128, 128) <= 256 || !aligned || a.N >= kMxTileMaxN)
-        launch_ring<true, 128, 128, 2, 2, 2, 8, 4>(a, stream);
+    else if (tiles(a, 128, 128) <= (aligned ? 256 : 512)) launch_ring<true, 128, 128, 2, 2, 2, 8, 4>(a, stream);
+    else if (!aligned) launch_ring<true, 256, 256, 2, 4, 1, 4, 4>(a, stream);
     else if (tiles(a, 128, 256) <= 256) launch_a4_tile<128, 256>(a, stream);
     else launch_a4_tile<256, 256>(a, stream);
     return hipGetLastError();
