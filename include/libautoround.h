@@ -215,7 +215,7 @@ AR_API ar_status ar_w4a16_gemm(const void* X, ar_dtype xt, int64_t M, int64_t K,
  * graph, and are stream-ordered without synchronization.  Common errors:
  * AR_ERR_INVALID_ARG for a NULL pointer, negative rows or a K that is no
  * positive multiple of 32; AR_ERR_UNSUPPORTED for K >= 2^30 (products:
- * 2^23), more than 2^34 elements (2^40 of Y) or a pointer that is not 16-byte
+ * 2^23), more than 2^34 elements (2^37 of Y) or a pointer that is not 16-byte
  * aligned (scales and Y: any).
  * Outputs must not overlap inputs. */
 

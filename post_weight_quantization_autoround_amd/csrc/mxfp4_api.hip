@@ -34,7 +34,8 @@ ar_status check_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* packed, con
     st = check_shape("N", N, "K", K);
     if (st != AR_OK) return st;
     // at most 2^34 / 32 rows on either side: the product of the two cannot overflow
-    if (M * N > (int64_t)1 << 40) return fail(AR_ERR_UNSUPPORTED, "Y may hold at most 2^40 elements");
+    // (2^37 outputs in tiles of at least 2^15 by 512 threads: fewer than 2^32 threads)
+    if (M * N > (int64_t)1 << 37) return fail(AR_ERR_UNSUPPORTED, "Y may hold at most 2^37 elements");
     if (K >= kMxGemmMaxK) return fail(AR_ERR_UNSUPPORTED, "the products need K below %lld", (long long)kMxGemmMaxK);
     if (!packed || !scale) return fail(AR_ERR_INVALID_ARG, "packed and scale must be non-NULL");
     if (!dtype_ok(yt)) return fail(AR_ERR_INVALID_ARG, "unknown output dtype");
@@ -79,7 +80,6 @@ ar_status ar_rmsnorm_mxfp4(const void* x, const void* delta, ar_dtype delta_dtyp
     if (st != AR_OK) return st;
     if (H > kMxNormMaxH) return fail(AR_ERR_UNSUPPORTED, "H must be at most %lld, got %lld", (long long)kMxNormMaxH,
                                      (long long)H);
-    if (M > ((int64_t)1 << 31) - 1) return fail(AR_ERR_UNSUPPORTED, "M must be below 2^31");
     if (delta && !dtype_ok(delta_dtype)) return fail(AR_ERR_INVALID_ARG, "unknown delta dtype");
     if (!(eps >= 0.0f)) return fail(AR_ERR_INVALID_ARG, "eps must be >= 0");
     if (M == 0) return AR_OK;

@@ -381,10 +381,23 @@ hipError_t launch_mx_rmsnorm(const MxNormArgs& a, hipStream_t stream) {
     int ch = a.M > 512 ? 2 : 1;
     while (chunks > 1024 * ch) ch *= 2;
     const int nt = (int)(((chunks + ch - 1) / ch + 63) / 64) * 64;
-    if (ch == 1) launch_norm<1>(a, nt, stream);
-    else if (ch == 2) launch_norm<2>(a, nt, stream);
-    else launch_norm<4>(a, nt, stream);
-    return hipGetLastError();
+    const int64_t most = ((int64_t)1 << 31) / nt;   // rows of one launch: a grid has fewer than 2^32 threads
+    for (int64_t m = 0; m < a.M; m += most) {
+        MxNormArgs s = a;
+        const int64_t d = m * a.H;
+        s.M = a.M - m < most ? a.M - m : most;
+        s.x += d;
+        if (a.delta) s.delta = static_cast<const uint8_t*>(a.delta) + d * (a.delta_bf16 ? 2 : 4);
+        if (a.r_out) s.r_out += d;
+        s.packed += d >> 3;
+        s.scale += d >> 5;
+        if (ch == 1) launch_norm<1>(s, nt, stream);
+        else if (ch == 2) launch_norm<2>(s, nt, stream);
+        else launch_norm<4>(s, nt, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_mx_swiglu(const MxGateArgs& a, hipStream_t stream) {

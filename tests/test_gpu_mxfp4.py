@@ -308,6 +308,39 @@ def test_products_general(ar, m, n, k):
         assert (err <= tol + U8 * (np.abs(ref) + tol)).all()
 
 
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_products_of_subnormal_values(ar, m):
+    # X below bf16's smallest normal number times a weight of 2^120, and a weight of 2^-127 and 2^-128 (scale byte 0)
+    # times an X of 2^120: products around 2^-8, exact sums
+    n, k = 70, 320
+    rng = np.random.default_rng(m)
+    codes = rng.integers(0, 3, (n, k)).astype(np.uint8)                     # 0, 0.5, 1
+    ints = rng.integers(-7, 8, (m, k)).astype(F32)
+    for byte, unit in ((247, 2.0 ** -130), (0, 2.0 ** 120)):
+        wp, ws = mx.pack(codes), np.full((n, k // 32), byte, np.uint8)
+        X = (ints.astype(np.float64) * unit).astype(F32)
+        ref = (X.astype(np.float64) @ mx.values(wp, ws).T).astype(F32)
+        assert np.abs(ref).max() > 2.0 ** -12
+        np.testing.assert_array_equal(_np(ar.mxfp4_gemm(_dev(X, True), _dev(wp), _dev(ws))), ref)
+
+
+def test_rmsnorm_of_more_rows_than_a_launch_holds(ar):
+    m, h = (1 << 25) + 1000, 32                       # 64 threads a row: 2^31 threads and some
+    x = torch.zeros((m, h), dtype=torch.bfloat16, device="cuda")
+    rows = [0, (1 << 25) - 1, 1 << 25, m - 1]
+    rng = np.random.default_rng(3)
+    part = to_bf16_values(rng.standard_normal((len(rows), h)).astype(F32))
+    x[rows] = _dev(part, True)
+    d = torch.zeros((m, h), dtype=torch.bfloat16, device="cuda")
+    d[rows] = _dev(part, True)
+    packed, scale, r = ar.rmsnorm_mxfp4(x, delta=d, delta_scale=0.5)
+    rr = mx.residual(part, part, 0.5)
+    codes, sc = mx.quantize(mx.rmsnorm(rr, None, 1e-5))
+    _same_packed((packed[rows], scale[rows]), codes, sc)
+    np.testing.assert_array_equal(_np(r[rows]), to_bf16_values(rr))
+    assert int(packed.count_nonzero()) == int(packed[rows].count_nonzero())
+
+
 @pytest.mark.parametrize("m", [1, 16, 40, 130, 600])
 def test_products_write_their_output_only(ar, m):
     n, k = 261, 160
