@@ -66,7 +66,7 @@ __device__ __forceinline__ void mx_tile(uint32_t tiles_m, uint32_t tiles_n, uint
 }
 
 // ------------------------------------------------------- few rows of X ----
-// Up to 16 rows: streaming the weight once is the bound.  No LDS staging; a
+// A few rows (16 at most): streaming the weight once is the bound.  No LDS staging; a
 // workgroup of 16 wavefronts owns 16 weight rows and its wavefronts take the
 // super-steps of 128 k in turn, two per round with all loads issued first.
 // Partial sums meet in LDS in wave order.  A lane holds row l % 16 and block
@@ -479,8 +479,10 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     constexpr int STAGE = XB + BN * WB > RED ? XB + BN * WB : RED;
     using SX = ScaleRing<BM, SB * NST, NW>;
     using SW = ScaleRing<BN, SB * NST, NW>;
-    __shared__ __attribute__((aligned(1024))) char st0[STAGE], st1[STAGE], st2[STAGE], st3[NST > 3 ? STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) char st0[STAGE], st1[STAGE], st2[STAGE], st3[NST > 3 ? STAGE : 16],
+        st4[NST > 4 ? STAGE : 16], st5[NST > 5 ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) char ssw[2 * SW::BYTES], ssx[A4 ? 2 * SX::BYTES : 16];
+    static_assert(NST >= 3 && NST <= 6, "the buffers above");
     static_assert(SPW * NWK == STEPS, "the steps of a stage split over the sets");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wk = wave % NWK, wn = wave / NWK % NWN, wm = wave / (NWK * NWN), r = lane & 31, half = lane >> 5;
@@ -601,7 +603,9 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
         if constexpr (p == 0) return st0;
         else if constexpr (p == 1) return st1;
         else if constexpr (p == 2) return st2;
-        else return st3;
+        else if constexpr (p == 3) return st3;
+        else if constexpr (p == 4) return st4;
+        else return st5;
     };
     issue_scales(0);
     gemm::static_for<NST - 1>([&](auto S) { issue(decltype(S)::value, buf(S)); });
@@ -703,20 +707,28 @@ void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
 // it latency, so one round of small tiles beats a part-filled round of large
 // ones, and with several rounds what counts is how often a tile re-reads its
 // operands.  Measured (us, the choice first):
-//   bf16 X: 16 x 28672 x 8192 32x128 29, 32x64 34, 64x128 39; 64 x 4096 x 4096
-//   32x64 10, 64x64 14; 130 x 4096 x 11008 64x64 30, 64x128 39; 256 x 11008 x
-//   4096 64x128 in two rounds 36, 64x64 41, 128x256 54; 512 x 11008 x 4096
-//   128x256 55, 64x128 58; 2048 x 11008 x 4096 128x256 168, 256x256 182; 8192 x
-//   8192 x 8192 256x256 780 (1.41 PFLOP/s), 128x256 831
-//   packed X: 16 x 28672 x 8192 32x64 27, 32x32 31, 32x128 32; 64 x 4096 x 4096
-//   32x32 6.0, 32x64 7.4; 130 x 4096 x 11008 64x64 16, 32x64 20, 64x128 21; 256 x
-//   11008 x 4096 128x128 17, 128x256 20; 512 x 11008 x 4096 128x256 22, 256x256
-//   29, 128x128 31; 1024 x 11008 x 4096 256x256 33, 128x256 43
-// Up to 16 rows on up to 4096 outputs (one workgroup of 16 a CU) take the
-// skinny kernel, which has no ring to fill: 1 x 4096 x 11008 9.4 against 24
-// (bf16), 7.9 against 11 (packed).
+//   bf16 X: 16 x 8192 x 28672 32x32 40-43, 32x64 56; 16 x 28672 x 8192 32x128 29,
+//   32x64 34, 64x128 39; 64 x 4096 x 4096 32x32 8.8, 32x64 10, 64x64 14; 130 x
+//   4096 x 11008 64x64 30, 64x128 39; 256 x 11008 x 4096 64x128 in two rounds 36,
+//   64x64 41, 128x256 54; 512 x 11008 x 4096 128x256 55, 64x128 58; 2048 x 11008 x
+//   4096 128x256 168, 256x256 182; 8192 x 8192 x 8192 256x256 780 (1.41 PFLOP/s),
+//   128x256 831
+//   packed X: 16 x 8192 x 28672 32x32 of six stages 28, of four 35; 16 x 28672 x
+//   8192 32x64 27, 32x32 31, 32x128 32; 64 x 4096 x 4096 32x32 6.2, 32x64 7.4; 130
+//   x 4096 x 11008 64x64 16, 32x64 20, 64x128 21; 256 x 11008 x 4096 128x128 17,
+//   128x256 20; 512 x 11008 x 4096 128x256 22, 256x256 29, 128x128 31; 1024 x 11008
+//   x 4096 256x256 33, 128x256 43
+// A few rows on up to 4096 outputs (one workgroup of 16 a CU) take the skinny
+// kernel, which has no ring to fill, but loads X's rows once for every 16 outputs:
+//   bf16 X, rows x 4096 x 11008: 1 row 9.3 against 15.3, 12 rows 15.1 against
+//   15.5, 16 rows 16.9 against 15.4 (1024 x 8192: 1 row 7.6 and 11.8, 16 rows 13.4
+//   and 11.9), so up to 12 rows
+//   packed X, a quarter of the bytes: 1 row 7.9 against 10.5, 16 rows 9.8 against
+//   10.5 (1024 x 8192: 6.4 and 8.2, 9.4 and 8.3), so up to the 16 rows it holds
+// With 8192 outputs the ring is as fast for one row (1 x 8192 x 8192 12.8 against 13.5).
 hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
-    if (a.M <= 16 && a.N <= 4096) launch_skinny<false>(a, stream);
+    if (a.M <= 12 && a.N <= 4096) launch_skinny<false>(a, stream);
+    else if (tiles(a, 32, 32) <= 256) launch_ring<false, 32, 32, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 32, 64) <= 256) launch_ring<false, 32, 64, 1, 2, 2, 8, 3>(a, stream);
     else if (a.M <= 32) launch_ring<false, 32, 128, 1, 2, 2, 8, 4>(a, stream);
     else if (tiles(a, 64, 64) <= 256) launch_ring<false, 64, 64, 1, 1, 4, 8, 3>(a, stream);
@@ -739,7 +751,7 @@ hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream) {
     const bool aligned = a.K % 128 == 0 && a.K >= 256 && a.N < kMxTileMaxN &&
                          ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
     if (a.M <= 16 && a.N <= 4096) launch_skinny<true>(a, stream);
-    else if (tiles(a, 32, 32) <= 256) launch_ring<true, 32, 32, 1, 1, 4, 8, 4>(a, stream);
+    else if (tiles(a, 32, 32) <= 256) launch_ring<true, 32, 32, 1, 1, 4, 8, 6>(a, stream);
     else if (tiles(a, 32, 64) <= 256 || a.M <= 32) launch_ring<true, 32, 64, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 64, 64) <= 256) launch_ring<true, 64, 64, 1, 1, 4, 8, 4>(a, stream);
     else if (tiles(a, 64, 128) <= 256) launch_ring<true, 64, 128, 1, 2, 2, 8, 4>(a, stream);

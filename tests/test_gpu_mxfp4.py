@@ -229,7 +229,8 @@ def test_products_exact(ar, m, n, k):
 # K that does not, rows of scales on and off dword boundaries.
 TILED = [(17, 9000, 96), (17, 20000, 1056), (40, 5000, 288), (130, 4200, 416), (130, 4200, 1024), (130, 9000, 288),
          (300, 9000, 160), (300, 9000, 640), (300, 17000, 288), (300, 17000, 384), (520, 17000, 288), (520, 17000, 768),
-         (520, 17000, 128), (600, 9000, 352), (1100, 8000, 96), (1100, 8000, 1088), (2000, 8300, 160), (2000, 8300, 512)]
+         (520, 17000, 128), (600, 9000, 352), (1100, 8000, 96), (1100, 8000, 1088), (2000, 8300, 160), (2000, 8300, 512),
+         (12, 900, 736), (13, 900, 736), (17, 1000, 32), (20, 1500, 5088), (33, 3000, 8224), (5, 8000, 1376)]
 
 
 @pytest.mark.parametrize("m,n,k", TILED)
