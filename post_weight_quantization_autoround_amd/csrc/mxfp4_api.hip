@@ -1,5 +1,7 @@
 // C ABI of the packed-MXFP4 operators: host checks, then one launch each.
 // Nothing is allocated.
+#include <initializer_list>
+
 #include "mxfp4.h"
 #include "tuner.h"
 
@@ -19,6 +21,27 @@ ar_status check_shape(const char* rn, int64_t rows, const char* cn, int64_t cols
         return fail(AR_ERR_INVALID_ARG, "%s must be a multiple of 32 (the MXFP4 block), got %lld", cn, (long long)cols);
     if (cols >= ((int64_t)1 << 30)) return fail(AR_ERR_UNSUPPORTED, "%s must be below 2^30", cn);
     if (rows > kMaxElems / cols) return fail(AR_ERR_UNSUPPORTED, "problem too large");
+    return AR_OK;
+}
+
+struct Span {
+    const void* p;   // nullable: not there
+    int64_t bytes;
+};
+
+// Outputs overlap no input and no other output: workgroups read what others
+// have not finished with in no fixed order.
+ar_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    auto meet = [](const Span& a, const Span& b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && (x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes);
+    };
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            if (meet(*o, i)) return fail(AR_ERR_INVALID_ARG, "an output overlaps an input");
+        for (const Span* q = outs.begin(); q != o; ++q)
+            if (meet(*o, *q)) return fail(AR_ERR_INVALID_ARG, "two outputs overlap");
+    }
     return AR_OK;
 }
 
@@ -56,6 +79,9 @@ ar_status ar_pack_mxfp4(const void* W, ar_dtype wt, int64_t N, int64_t K, const 
     if (!W || !packed || !scale) return fail(AR_ERR_INVALID_ARG, "W, packed and scale must be non-NULL");
     if (!aligned(W, 16) || !aligned(packed, 16))
         return fail(AR_ERR_UNSUPPORTED, "W and packed must be 16-byte aligned");
+    st = check_apart({{packed, N * K / 2}, {scale, N * K / 32}},
+                     {{W, N * K * (wt == AR_BF16 ? 2 : 4)}, {alpha, N * K / 8}});
+    if (st != AR_OK) return st;
     MxPackArgs a{W, wt == AR_BF16, N * (K / 32), alpha, reinterpret_cast<uint32_t*>(packed), scale};
     return launched(launch_mx_pack(a, static_cast<hipStream_t>(stream)), "MXFP4 pack");
 }
@@ -69,6 +95,8 @@ ar_status ar_unpack_mxfp4(const uint8_t* packed, const uint8_t* scale, int64_t N
     if (!W || !packed || !scale) return fail(AR_ERR_INVALID_ARG, "packed, scale and W must be non-NULL");
     if (!aligned(W, 16) || !aligned(packed, 16))
         return fail(AR_ERR_UNSUPPORTED, "packed and W must be 16-byte aligned");
+    st = check_apart({{W, N * K * (wt == AR_BF16 ? 2 : 4)}}, {{packed, N * K / 2}, {scale, N * K / 32}});
+    if (st != AR_OK) return st;
     MxUnpackArgs a{reinterpret_cast<const uint32_t*>(packed), scale, N * (K / 32), W, wt == AR_BF16};
     return launched(launch_mx_unpack(a, static_cast<hipStream_t>(stream)), "MXFP4 unpack");
 }
@@ -86,6 +114,9 @@ ar_status ar_rmsnorm_mxfp4(const void* x, const void* delta, ar_dtype delta_dtyp
     if (!x || !packed || !scale) return fail(AR_ERR_INVALID_ARG, "x, packed and scale must be non-NULL");
     if (!aligned(x, 16) || !aligned(delta, 16) || !aligned(w, 16) || !aligned(r_out, 16) || !aligned(packed, 16))
         return fail(AR_ERR_UNSUPPORTED, "x, delta, w, r_out and packed must be 16-byte aligned");
+    st = check_apart({{r_out, 2 * M * H}, {packed, M * H / 2}, {scale, M * H / 32}},
+                     {{x, 2 * M * H}, {delta, M * H * (delta_dtype == AR_BF16 ? 2 : 4)}, {w, 4 * H}});
+    if (st != AR_OK) return st;
     MxNormArgs a{};
     a.x = static_cast<const uint16_t*>(x);
     a.delta = delta; a.delta_bf16 = (delta_dtype == AR_BF16); a.delta_scale = delta_scale;
@@ -105,6 +136,9 @@ ar_status ar_swiglu_mxfp4(const void* gate, int64_t ld_gate, const void* up, int
         return fail(AR_ERR_INVALID_ARG, "gate, up, packed and scale must be non-NULL");
     if (ld_gate % 8 != 0 || ld_up % 8 != 0 || !aligned(gate, 16) || !aligned(up, 16) || !aligned(packed, 16))
         return fail(AR_ERR_UNSUPPORTED, "gate, up and packed must be 16-byte aligned and the row strides multiples of 8");
+    st = check_apart({{packed, M * F / 2}, {scale, M * F / 32}},
+                     {{gate, 2 * ((M - 1) * ld_gate + F)}, {up, 2 * ((M - 1) * ld_up + F)}});
+    if (st != AR_OK) return st;
     MxGateArgs a{static_cast<const uint16_t*>(gate), ld_gate, static_cast<const uint16_t*>(up), ld_up, M, F,
                  reinterpret_cast<uint32_t*>(packed), scale};
     return launched(launch_mx_swiglu(a, static_cast<hipStream_t>(stream)), "MXFP4 SwiGLU");
@@ -117,6 +151,9 @@ ar_status ar_mxfp4_gemm(const void* X, int64_t M, int64_t K, const uint8_t* pack
     if (M == 0) return AR_OK;
     if (!X || !Y) return fail(AR_ERR_INVALID_ARG, "X and Y must be non-NULL when M > 0");
     if (!aligned(X, 16)) return fail(AR_ERR_UNSUPPORTED, "X must be 16-byte aligned");
+    st = check_apart({{Y, M * N * (yt == AR_BF16 ? 2 : 4)}},
+                     {{X, 2 * M * K}, {packed, N * K / 2}, {scale, N * K / 32}});
+    if (st != AR_OK) return st;
     MxGemmArgs a{};
     a.x = static_cast<const uint16_t*>(X);
     a.wp = packed; a.ws = scale; a.M = M; a.N = N; a.K = K; a.y = Y; a.y_bf16 = (yt == AR_BF16);
@@ -132,6 +169,9 @@ ar_status ar_mxfp4_gemm_a4(const uint8_t* x_packed, const uint8_t* x_scale, int6
     if (!x_packed || !x_scale || !Y)
         return fail(AR_ERR_INVALID_ARG, "x_packed, x_scale and Y must be non-NULL when M > 0");
     if (!aligned(x_packed, 16)) return fail(AR_ERR_UNSUPPORTED, "x_packed must be 16-byte aligned");
+    st = check_apart({{Y, M * N * (yt == AR_BF16 ? 2 : 4)}},
+                     {{x_packed, M * K / 2}, {x_scale, M * K / 32}, {packed, N * K / 2}, {scale, N * K / 32}});
+    if (st != AR_OK) return st;
     MxGemmArgs a{};
     a.xp = x_packed; a.xs = x_scale;
     a.wp = packed; a.ws = scale; a.M = M; a.N = N; a.K = K; a.y = Y; a.y_bf16 = (yt == AR_BF16);

@@ -488,6 +488,18 @@ def test_captured_graph_and_other_streams(ar, m):
     del graph
 
 
+def test_out_over_an_operand_is_refused(ar):
+    x = torch.ones((64, 64), dtype=torch.bfloat16, device="cuda")
+    p, s = ar.pack_mxfp4(x)
+    with pytest.raises(ar.ARError, match="overlaps"):
+        ar.mxfp4_gemm(x, p, s, out_dtype=torch.bfloat16, out=x)
+    both = torch.empty((3, 64, 64), dtype=torch.bfloat16, device="cuda")   # neighbours in one allocation are no overlap
+    both[1] = 1
+    ar.mxfp4_gemm(both[1], p, s, out_dtype=torch.bfloat16, out=both[0])
+    ar.mxfp4_gemm(both[1], p, s, out_dtype=torch.bfloat16, out=both[2])
+    assert (both[0] == 64).all() and (both[2] == 64).all() and (both[1] == 1).all()
+
+
 def test_binding_refusals(ar):
     x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
     p, s = ar.pack_mxfp4(x)

@@ -74,6 +74,39 @@ def test_refused(ar, name, kw, expect):
     assert ar.lib.ar_last_error().decode()
 
 
+def _at(byte):
+    return ctypes.c_void_p(byte)
+
+
+APART = {      # operands of _call's sizes, well apart
+    "ar_pack_mxfp4": dict(W=0x10000, alpha=0x20000, packed=0x30000, scale=0x40000),
+    "ar_unpack_mxfp4": dict(packed=0x10000, scale=0x20000, W=0x30000),
+    "ar_rmsnorm_mxfp4": dict(x=0x10000, delta=0x20000, w=0x30000, r=0x40000, packed=0x50000, scale=0x60000),
+    "ar_swiglu_mxfp4": dict(gate=0x10000, up=0x20000, packed=0x30000, scale=0x40000),
+    "ar_mxfp4_gemm": dict(X=0x10000, packed=0x20000, scale=0x30000, Y=0x40000),
+    "ar_mxfp4_gemm_a4": dict(xp=0x10000, xs=0x20000, packed=0x30000, scale=0x40000, Y=0x50000),
+}
+OVERLAPS = [   # (call, output, operand it meets, that operand's bytes)
+    ("ar_pack_mxfp4", "packed", "W", 512), ("ar_pack_mxfp4", "scale", "alpha", 32),
+    ("ar_pack_mxfp4", "scale", "packed", 128), ("ar_unpack_mxfp4", "W", "packed", 128),
+    ("ar_unpack_mxfp4", "W", "scale", 8), ("ar_rmsnorm_mxfp4", "r", "x", 512), ("ar_rmsnorm_mxfp4", "r", "delta", 512),
+    ("ar_rmsnorm_mxfp4", "packed", "w", 256), ("ar_rmsnorm_mxfp4", "scale", "r", 512),
+    ("ar_swiglu_mxfp4", "packed", "gate", 512), ("ar_swiglu_mxfp4", "scale", "up", 512),
+    ("ar_mxfp4_gemm", "Y", "X", 512), ("ar_mxfp4_gemm", "Y", "packed", 256), ("ar_mxfp4_gemm", "Y", "scale", 16),
+    ("ar_mxfp4_gemm_a4", "Y", "xp", 128), ("ar_mxfp4_gemm_a4", "Y", "xs", 8),
+]
+
+
+@pytest.mark.parametrize("name,out,other,size", OVERLAPS)
+def test_overlaps_are_refused(ar, name, out, other, size):
+    # from the operand's first 16 bytes on, and with its last ones
+    for at in (APART[name][other], APART[name][other] + max(0, (size - 1) // 16 * 16)):
+        kw = {k: _at(v) for k, v in APART[name].items()}
+        kw[out] = _at(at)
+        assert _call(ar, name, **kw) == INVALID
+        assert b"overlap" in ar.lib.ar_last_error()
+
+
 @pytest.mark.parametrize("name,kw", [
     ("ar_pack_mxfp4", dict(N=0, W=None, packed=None, scale=None)),
     ("ar_unpack_mxfp4", dict(N=0, W=None, packed=None, scale=None)),
