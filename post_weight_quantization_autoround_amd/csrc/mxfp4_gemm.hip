@@ -66,7 +66,7 @@ __device__ __forceinline__ void mx_tile(uint32_t tiles_m, uint32_t tiles_n, uint
 }
 
 // ------------------------------------------------------- few rows of X ----
-// A few rows (16 at most): streaming the weight once is the bound.  No LDS staging; a
+// 16 rows at most: streaming the weight once is the bound.  No LDS staging; a
 // workgroup of 16 wavefronts owns 16 weight rows and its wavefronts take the
 // super-steps of 128 k in turn, two per round with all loads issued first.
 // Partial sums meet in LDS in wave order.  A lane holds row l % 16 and block
