@@ -307,9 +307,11 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(MxNormArgs a) {
 // 4096 x 28672: 103 us, 5.2 TB/s of what has to move: HBM's rate.
 // h = g / (1 + exp(-g)) u.  Fast path: exp(-g) = 2^(-g log2 e) by v_exp_f32
 // and v_rcp_f32.  Its error is that of the exponent's product, |g| 2^-23.7
-// relative for g < 0 (below 2^-17.2 for |g| <= 88; past that h is below
-// 2^-100 times the block maximum or the block is recomputed), plus a few
-// units of 2^-23.
+// relative for g < 0 (below 2^-17.2 down to g = -87.3), plus a few units of
+// 2^-23.  Below -87.3 the reciprocal leaves fp32's normal range (and is 0 from
+// -88.7 on).  There |g / (1 + exp(-g))| < 2^-119.5, so with |u| <= 2^15 h stays
+// under 2^-104, a quarter of the smallest 2^e that the fast path takes, and its
+// code is 0 however it comes out; with a larger |u| the block is recomputed.
 // Chunks of 8 are numbered across rows; a chunk's row is c / per_row by a
 // multiplication (c < 2^31, magic = ceil(2^(31 + l) / per_row) with l =
 // ceil(log2 per_row), whose excess over the quotient is below 1 / per_row).
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kThreads) mx_swiglu_kernel(MxGateArgs a, uint3
     const u32x4 gd = *reinterpret_cast<const u32x4*>(a.gate + row * a.ld_gate + col);
     const u32x4 ud = *reinterpret_cast<const u32x4*>(a.up + row * a.ld_up + col);
     float g[8], u[8], h[8];
-    uint32_t src = 0;
+    uint32_t src = 0, low = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         g[2 * i] = lo_f32(gd[i]);
@@ -336,9 +338,15 @@ __global__ void __launch_bounds__(kThreads) mx_swiglu_kernel(MxGateArgs a, uint3
         const float ex = __builtin_amdgcn_exp2f(g[i] * -1.44269504f);
         h[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + ex) * u[i];
         src |= (g[i] != 0.0f && u[i] != 0.0f) ? 1u : 0u;
+        low = max_u32(low, __float_as_uint(g[i]));   // of the negative ones, the lowest
+    }
+    bool deep = false;
+    if (low > __float_as_uint(-87.0f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) deep |= abs_bits(u[i]) > __float_as_uint(32768.0f);
     }
     uint32_t code, byte;
-    if (__any(quantize_guarded(h, D, src, code, byte))) {
+    if (__any(quantize_guarded(h, D, src, code, byte) || deep)) {
         double h64[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) h64[i] = (double)g[i] / (1.0 + exp(-(double)g[i])) * (double)u[i];

@@ -191,6 +191,33 @@ def test_swiglu_hard_values(ar):
     _same_packed(ar.swiglu_mxfp4(_dev(g, True), _dev(u, True)), codes, scale, "nonfinite")
 
 
+def test_swiglu_factors_past_the_fp32_range(ar):
+    # blocks that mix ordinary elements with ones whose sigmoid or g sigmoid(g) leaves fp32's normal range (gates around
+    # -88 and far below, subnormal gates) and whose factor brings the product back among the others
+    g = np.zeros((4, 32), F32)
+    u = np.zeros((4, 32), F32)
+    g[0, :2], u[0, :2] = (1, -90), (1, 1e38)
+    g[1], u[1] = 1, 1
+    g[1, 7], u[1, 7] = -90, 2.0 ** 125
+    g[2], u[2] = 1.3 * 2.0 ** -20, 1.3 * 2.0 ** -20
+    g[2, 3], u[2, 3] = 1.71875 * 2.0 ** -131, 1.40625 * 2.0 ** 89
+    g[3], u[3] = 1, 1
+    g[3, 9], u[3, 9] = -88, -1.25 * 2.0 ** 122
+    rng = np.random.default_rng(11)
+    m, f = 64, 512
+    gr = rng.standard_normal((m, f)) * 4
+    ur = rng.standard_normal((m, f)) * 2.0 ** rng.integers(-40, 20, (m, f // 32)).repeat(32, axis=1)
+    deep = rng.random((m, f)) < 0.05
+    tiny = rng.random((m, f)) < 0.5
+    far = np.where(tiny, np.sign(gr) * 2.0 ** rng.uniform(-133, -100, (m, f)), rng.uniform(-130, -80, (m, f)))
+    gr = np.where(deep, far, gr)
+    ur = np.where(deep, np.sign(ur) * 2.0 ** rng.uniform(60, 127.9, (m, f)), ur)
+    for i, (gate, up) in enumerate([(g[j:j + 1], u[j:j + 1]) for j in range(4)] + [(gr, ur)]):
+        gate, up = to_bf16_values(gate.astype(F32)), to_bf16_values(up.astype(F32))
+        codes, scale = mx.quantize(mx.swiglu(gate, up))
+        _same_packed(ar.swiglu_mxfp4(_dev(gate, True), _dev(up, True)), codes, scale, f"set {i}")
+
+
 # --------------------------------------------------------------- products
 SHAPES = [(1, 1, 32), (1, 16, 64), (1, 4096, 4096), (2, 33, 96), (3, 100, 160), (15, 17, 128), (16, 256, 2048),
           (17, 129, 288), (31, 64, 512), (32, 1000, 2080), (33, 96, 4096), (64, 130, 256), (65, 48, 1120),
