@@ -215,7 +215,11 @@ __device__ __forceinline__ bool quantize_guarded(const float h[8], float D, uint
 // delta are read once (2048 x 8192 with a bf16 delta: 22 us, 4.9 TB/s of what
 // has to move, HBM's rate).  The squares are summed in fp64: the fast path's h
 // then differs from the fp64 value by the roundings of 1/rms to fp32 and of
-// two products, 3 * 2^-24 in all.
+// two products, 3 * 2^-24 in all (2^-22 + 2 * 2^-24 where 1/rms is subnormal).
+// Where r/rms itself is below 2^-126 the relative error has no such bound: with
+// |w| <= 2^16 h then stays under 2^-109, too small for any code but 0 in a block
+// that the fast path takes (a maximum of 2^-100 or more); blocks with a larger
+// |w| are recomputed.
 template <int CH, int DELTA>   // DELTA: 0 none, 1 bf16, 2 fp32
 __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(MxNormArgs a) {
     constexpr float D = 0x1p-21f;
@@ -285,8 +289,9 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(MxNormArgs a) {
             h[i] = r[j][i] * inv * w[i];
             src |= abs_bits(r[j][i]);
         }
+        const bool wide = max_abs_bits(w) > __float_as_uint(65536.0f);
         uint32_t code, byte;
-        if (__any(quantize_guarded(h, D, src, code, byte))) {
+        if (__any(quantize_guarded(h, D, src, code, byte) || wide)) {
             double h64[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) h64[i] = (double)r[j][i] / rms * (double)w[i];

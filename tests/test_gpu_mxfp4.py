@@ -158,6 +158,25 @@ def test_rmsnorm_hard_rows(ar):
             _same_packed(got, codes, scale, f"eps {eps} weight {ww is not None}")
 
 
+def test_rmsnorm_weights_past_the_fp32_range(ar):
+    # an element of 2^100 (its normalized value, sqrt(96), is near no border) brings r / rms of the others below fp32's
+    # normal range, and weights bring them back: a block of them, and single ones beside ordinary elements
+    rng = np.random.default_rng(12)
+    m, h = 64, 96
+    x = rng.choice([-1.0, 1.0], (m, h)) * rng.uniform(1, 2, (m, h))
+    w = np.ones(h)
+    x[:, 0], x[:, 1:32] = 2.0 ** 100, 0
+    x[:, 32:64] *= 2.0 ** rng.integers(-54, -45, (m, 1))
+    w[32:64] = rng.uniform(3e29, 1e30, 32)
+    x[:, 70:90:5] *= 2.0 ** -60
+    w[70:90:5] = 2.0 ** 120 * rng.uniform(1, 2, 4)
+    x[0, 32:64] = 1.71875 * 2.0 ** -50
+    x = to_bf16_values(x.astype(F32))
+    w = w.astype(F32)
+    codes, scale = mx.quantize(mx.rmsnorm(x, w, 1e-5))
+    _same_packed(ar.rmsnorm_mxfp4(_dev(x, True), weight=_dev(w), eps=1e-5), codes, scale)
+
+
 # ----------------------------------------------------------------- SwiGLU
 @pytest.mark.parametrize("m,f,joined", [(1, 32, False), (1, 11008, True), (7, 96, True), (33, 2080, False),
                                         (130, 1024, True)])
