@@ -293,6 +293,40 @@ def test_products_exact_over_the_tiles(ar, m, n, k):
         assert torch.equal(ar.mxfp4_gemm_a4(xp, xs, wp, ws, out_dtype=dt), want.to(dt))
 
 
+# Every tile again with K of several turns of its ring and a rest, and of whole turns in two tile columns at least (which
+# start at a turn of their own, also where the last stage ends early); the two tile kernels of packed operands with
+# more than one group of scales, K an odd and an even multiple of 128.
+TURNS = [(20, 1500, 2016), (20, 1500, 2400), (20, 1500, 4608), (20, 1500, 3616), (17, 9000, 1504), (17, 9000, 1888),
+         (17, 9000, 2400), (20, 20000, 2016), (20, 20000, 2400), (130, 4200, 1504), (130, 4200, 1888), (130, 4200, 2400),
+         (130, 9000, 1504), (130, 9000, 1888), (130, 9000, 2400), (300, 9000, 2016), (300, 9000, 2400),
+         (300, 17000, 2304), (300, 17000, 2432), (520, 17000, 2304), (520, 17000, 2432), (520, 17000, 992),
+         (520, 17000, 1184), (2000, 8300, 1152), (2000, 8300, 1184)]
+
+
+@pytest.mark.parametrize("m,n,k", TURNS)
+def test_products_exact_over_turns_of_the_ring(ar, m, n, k):
+    # operands as _exact_operand's, K < 7281; fp64 products and sums of them are exact
+    rng = np.random.default_rng(m + 3 * n + 7 * k)
+    table = _dev(mx.values(np.arange(16, dtype=np.uint8)[None], np.full((1, 1), 127, np.uint8)))[0, 0::2]
+
+    def operand(rows):
+        packed = rng.integers(0, 256, (rows, k // 2), np.uint8)
+        packed[packed % 16 == 8] &= 0xF0
+        packed[packed // 16 == 8] &= 0x0F
+        packed, scale = _dev(packed), _dev(rng.integers(126, 129, (rows, k // 32)).astype(np.uint8))
+        v = table[torch.stack((packed & 15, packed >> 4), -1).reshape(rows, k).int()]
+        return packed, scale, v * torch.exp2(scale.double() - 127).repeat_interleave(32, dim=1)
+
+    wp, ws, W = operand(n)
+    xp, xs, X = operand(m)
+    want = (X @ W.t()).float()
+    for dt in (torch.float32, torch.bfloat16):
+        print(f"a16 {m}x{n}x{k} {dt}", flush=True)
+        assert torch.equal(ar.mxfp4_gemm(X.bfloat16(), wp, ws, out_dtype=dt), want.to(dt))
+        print(f"a4 {m}x{n}x{k} {dt}", flush=True)
+        assert torch.equal(ar.mxfp4_gemm_a4(xp, xs, wp, ws, out_dtype=dt), want.to(dt))
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 40, 32), (16, 300, 288), (40, 5000, 160), (130, 4200, 288), (300, 9000, 96),
                                    (300, 17000, 288), (520, 17000, 352), (1100, 8000, 96), (2000, 8300, 160)])
 def test_products_keep_rows_apart(ar, m, n, k):
