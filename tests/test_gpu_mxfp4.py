@@ -467,6 +467,27 @@ def test_products_carry_nan_and_infinity(ar, m):
             _np(ar.mxfp4_gemm_a4(_dev(xp), _dev(xs2), _dev(wp), _dev(ws2), out_dtype=dt)), want)
 
 
+@pytest.mark.parametrize("m,n,k", [(3, 140, 352), (12, 140, 2080), (16, 140, 320), (40, 5000, 288), (300, 140, 352),
+                                   (300, 9000, 160), (520, 9000, 416)])
+def test_products_carry_infinite_activations(ar, m, n, k):
+    # +inf and -inf in X times a weight of either sign is an infinity, times a code 0 NaN, both signs in a row meet in
+    # NaN; other rows stay as they are
+    rng = np.random.default_rng(m + n)
+    wp, ws = _exact_operand(rng, n, k)
+    xp, xs = _exact_operand(rng, m, k)
+    X, W = mx.values(xp, xs), mx.values(wp, ws)
+    X[0, k - 1], X[m - 1, 0], X[1, 40], X[1, k - 2] = np.inf, -np.inf, np.inf, -np.inf
+    want = np.where(np.isfinite(X), X, 0.0) @ W.T
+    with np.errstate(invalid="ignore"):
+        for i in (0, 1, m - 1):
+            want[i] = (X[i] * W).sum(axis=1)
+    assert np.isposinf(want).any() and np.isneginf(want).any() and np.isnan(want[[0, m - 1]]).any()
+    x16, W = _dev(X.astype(F32), True), (_dev(wp), _dev(ws))
+    for dt in (torch.float32, torch.bfloat16):
+        ref = want.astype(F32) if dt == torch.float32 else to_bf16_values(want.astype(F32))
+        np.testing.assert_array_equal(_np(ar.mxfp4_gemm(x16, *W, out_dtype=dt)), ref)
+
+
 def test_products_past_32_bit_offsets(ar):
     # Y of 4.5 G elements (18 GB of fp32): rows past element 2^32 against the first ones
     m, n, k = 140_000, 32_000, 32
