@@ -248,7 +248,9 @@ AR_API ar_status ar_rmsnorm_mxfp4(const void* x, const void* delta, ar_dtype del
 /* The gated activation in front of the down projection, h = silu(gate) * up,
  * silu(a) = a / (1 + exp(-a)), as packed MXFP4 with the codes of h in 64 bits.
  *  gate, up  DEVICE bf16 [M, F], rows ld_gate / ld_up elements apart (at least
- *            F, multiples of 8), so both may be halves of one [M, 2F] product */
+ *            F, multiples of 8, the last row at most 2^40 elements from the
+ *            first: AR_ERR_UNSUPPORTED beyond), so both may be halves of one
+ *            [M, 2F] product */
 AR_API ar_status ar_swiglu_mxfp4(const void* gate, int64_t ld_gate, const void* up, int64_t ld_up, int64_t M,
                           int64_t F, uint8_t* packed, uint8_t* scale, void* stream);
 

@@ -11,6 +11,7 @@ using namespace ar::rt;
 namespace {
 
 constexpr int64_t kMaxElems = (int64_t)1 << 34;
+constexpr int64_t kMaxReach = (int64_t)1 << 40;   // last row's distance in elements: more than any memory, and its bytes fit 64 bits
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -136,6 +137,8 @@ ar_status ar_swiglu_mxfp4(const void* gate, int64_t ld_gate, const void* up, int
         return fail(AR_ERR_INVALID_ARG, "gate, up, packed and scale must be non-NULL");
     if (ld_gate % 8 != 0 || ld_up % 8 != 0 || !aligned(gate, 16) || !aligned(up, 16) || !aligned(packed, 16))
         return fail(AR_ERR_UNSUPPORTED, "gate, up and packed must be 16-byte aligned and the row strides multiples of 8");
+    if (M > 1 && (ld_gate > kMaxReach / (M - 1) || ld_up > kMaxReach / (M - 1)))
+        return fail(AR_ERR_UNSUPPORTED, "a row stride reaches past 2^40 elements");
     st = check_apart({{packed, M * F / 2}, {scale, M * F / 32}},
                      {{gate, 2 * ((M - 1) * ld_gate + F)}, {up, 2 * ((M - 1) * ld_up + F)}});
     if (st != AR_OK) return st;

@@ -107,6 +107,15 @@ def test_overlaps_are_refused(ar, name, out, other, size):
         assert b"overlap" in ar.lib.ar_last_error()
 
 
+@pytest.mark.parametrize("ld", ["ldg", "ldu"])
+@pytest.mark.parametrize("m,stride", [(5, 1 << 62), (1 << 20, 1 << 43), (2, (1 << 40) + 8), (3, (1 << 63) - 8)])
+def test_strides_past_any_memory_are_refused(ar, ld, m, stride):
+    # (m rows of such a stride wrap around 64 bits, so nothing may be computed from them)
+    kw = {k: _at(v) for k, v in APART["ar_swiglu_mxfp4"].items()}
+    assert _call(ar, "ar_swiglu_mxfp4", M=m, **{ld: stride}, **kw) == UNSUPPORTED
+    assert b"stride" in ar.lib.ar_last_error()
+
+
 @pytest.mark.parametrize("name,kw", [
     ("ar_pack_mxfp4", dict(N=0, W=None, packed=None, scale=None)),
     ("ar_unpack_mxfp4", dict(N=0, W=None, packed=None, scale=None)),
