@@ -217,7 +217,7 @@ AR_API ar_status ar_w4a16_gemm(const void* X, ar_dtype xt, int64_t M, int64_t K,
  * positive multiple of 32 or an output that overlaps an input or another
  * output; AR_ERR_UNSUPPORTED for K >= 2^30 (products:
  * 2^23), more than 2^34 elements (2^37 of Y) or a pointer that is not 16-byte
- * aligned (scales and Y: any). */
+ * aligned (scales: any address; alpha and Y: aligned as their type). */
 
 /* Quantize W DEVICE [N, K] (fp32 or bf16) to packed MXFP4: the codes of
  * ar_qdq_rtn, two per byte.  alpha DEVICE fp32 [N, K/32] clip factors, m =

@@ -80,6 +80,7 @@ ar_status ar_pack_mxfp4(const void* W, ar_dtype wt, int64_t N, int64_t K, const 
     if (!W || !packed || !scale) return fail(AR_ERR_INVALID_ARG, "W, packed and scale must be non-NULL");
     if (!aligned(W, 16) || !aligned(packed, 16))
         return fail(AR_ERR_UNSUPPORTED, "W and packed must be 16-byte aligned");
+    if (!aligned(alpha, 4)) return fail(AR_ERR_UNSUPPORTED, "alpha must be 4-byte aligned");
     st = check_apart({{packed, N * K / 2}, {scale, N * K / 32}},
                      {{W, N * K * (wt == AR_BF16 ? 2 : 4)}, {alpha, N * K / 8}});
     if (st != AR_OK) return st;
@@ -153,7 +154,8 @@ ar_status ar_mxfp4_gemm(const void* X, int64_t M, int64_t K, const uint8_t* pack
     if (st != AR_OK) return st;
     if (M == 0) return AR_OK;
     if (!X || !Y) return fail(AR_ERR_INVALID_ARG, "X and Y must be non-NULL when M > 0");
-    if (!aligned(X, 16)) return fail(AR_ERR_UNSUPPORTED, "X must be 16-byte aligned");
+    if (!aligned(X, 16) || !aligned(Y, yt == AR_BF16 ? 2 : 4))
+        return fail(AR_ERR_UNSUPPORTED, "X must be 16-byte aligned and Y as its type");
     st = check_apart({{Y, M * N * (yt == AR_BF16 ? 2 : 4)}},
                      {{X, 2 * M * K}, {packed, N * K / 2}, {scale, N * K / 32}});
     if (st != AR_OK) return st;
@@ -171,7 +173,8 @@ ar_status ar_mxfp4_gemm_a4(const uint8_t* x_packed, const uint8_t* x_scale, int6
     if (M == 0) return AR_OK;
     if (!x_packed || !x_scale || !Y)
         return fail(AR_ERR_INVALID_ARG, "x_packed, x_scale and Y must be non-NULL when M > 0");
-    if (!aligned(x_packed, 16)) return fail(AR_ERR_UNSUPPORTED, "x_packed must be 16-byte aligned");
+    if (!aligned(x_packed, 16) || !aligned(Y, yt == AR_BF16 ? 2 : 4))
+        return fail(AR_ERR_UNSUPPORTED, "x_packed must be 16-byte aligned and Y as its type");
     st = check_apart({{Y, M * N * (yt == AR_BF16 ? 2 : 4)}},
                      {{x_packed, M * K / 2}, {x_scale, M * K / 32}, {packed, N * K / 2}, {scale, N * K / 32}});
     if (st != AR_OK) return st;

@@ -107,6 +107,18 @@ def test_overlaps_are_refused(ar, name, out, other, size):
         assert b"overlap" in ar.lib.ar_last_error()
 
 
+@pytest.mark.parametrize("name,kw", [
+    ("ar_pack_mxfp4", dict(alpha=0x20002)), ("ar_mxfp4_gemm", dict(Y=0x40002, yt=0)),
+    ("ar_mxfp4_gemm", dict(Y=0x40001, yt=1)), ("ar_mxfp4_gemm_a4", dict(Y=0x50001, yt=0)),
+    ("ar_mxfp4_gemm_a4", dict(Y=0x50003, yt=1)),
+])
+def test_addresses_off_the_type_are_refused(ar, name, kw):
+    full = {k: _at(v) for k, v in APART[name].items()}
+    full.update({k: _at(v) if k != "yt" else v for k, v in kw.items()})
+    assert _call(ar, name, **full) == UNSUPPORTED
+    assert b"aligned" in ar.lib.ar_last_error()
+
+
 @pytest.mark.parametrize("ld", ["ldg", "ldu"])
 @pytest.mark.parametrize("m,stride", [(5, 1 << 62), (1 << 20, 1 << 43), (2, (1 << 40) + 8), (3, (1 << 63) - 8)])
 def test_strides_past_any_memory_are_refused(ar, ld, m, stride):
