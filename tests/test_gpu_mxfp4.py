@@ -488,6 +488,30 @@ def test_products_carry_infinite_activations(ar, m, n, k):
         np.testing.assert_array_equal(_np(ar.mxfp4_gemm(x16, *W, out_dtype=dt)), ref)
 
 
+@pytest.mark.parametrize("m", [3, 300])
+def test_products_of_the_longest_rows(ar, m):
+    # the largest K; X is zero except for 500 columns spread over it, the first and the last block among them
+    n, k = 40, (1 << 23) - 32
+    rng = np.random.default_rng(m)
+    cols = np.unique(np.concatenate([np.arange(32), k - 32 + np.arange(32), rng.integers(0, k, 436)]))
+    wp, ws = _dev(rng.integers(0, 256, (n, k // 2), np.uint8)), torch.full((n, k // 32), 126, dtype=torch.uint8, device="cuda")
+    W = mx.unpack(wp[:, cols // 2].cpu().numpy())[:, cols % 2 + 2 * np.arange(len(cols))]
+    W = mx.values(mx.pack(np.pad(W, ((0, 0), (0, -len(cols) % 32)))), np.full((n, -(-len(cols) // 32)), 126, np.uint8))
+    codes = rng.integers(1, 8, (m, len(cols)))                       # 0.5 .. 6
+    X = np.array([0.5, 1, 1.5, 2, 3, 4, 6])[codes - 1]
+    want = (X @ W[:, :len(cols)].T).astype(F32)                      # multiples of 2^-3 of at most 500 * 18: exact
+    at = torch.from_numpy(cols).cuda()
+    x = torch.zeros((m, k), dtype=torch.uint8, device="cuda")
+    x[:, at] = _dev(codes.astype(np.uint8))
+    xp = x[:, 0::2] | (x[:, 1::2] << 4)
+    del x
+    xs = torch.full((m, k // 32), 127, dtype=torch.uint8, device="cuda")
+    x16 = ar.unpack_mxfp4(xp, xs, out_dtype=torch.bfloat16)
+    np.testing.assert_array_equal(_np(x16[:, at]), X)
+    np.testing.assert_array_equal(_np(ar.mxfp4_gemm(x16, wp, ws)), want)
+    np.testing.assert_array_equal(_np(ar.mxfp4_gemm_a4(xp, xs, wp, ws)), want)
+
+
 def test_products_past_32_bit_offsets(ar):
     # Y of 4.5 G elements (18 GB of fp32): rows past element 2^32 against the first ones
     m, n, k = 140_000, 32_000, 32
