@@ -203,9 +203,9 @@ AR_API ar_status ar_w4a16_gemm(const void* X, ar_dtype xt, int64_t M, int64_t K,
 /* Packed MXFP4: the deployment form of the format that ar_qdq_rtn evaluates
  * with AR_FMT_MXFP4, for weights and for activations.  Along a row of K
  * elements (K a multiple of 32) each block of 32 shares 2^e; with m =
- * max|x_b|, e = max(floor(log2 m) - 2, -127), 0 for m = 0.  An element is the
- * E2M1 value nearest x / 2^e (ties to the even code, saturating at 6, no
- * negative zero).
+ * max|x_b|, e = max(floor(log2 m) - 2, -127), 0 for an m that is 0 in fp32.
+ * An element is the E2M1 value nearest x / 2^e (ties to the even code,
+ * saturating at 6, no negative zero).
  *  packed  DEVICE uint8 [rows, K/2]: byte j of a row holds code 2j in its low
  *          nibble and code 2j+1 in its high nibble; 16-byte aligned
  *  scale   DEVICE uint8 [rows, K/32]: e + 127; 255 (codes 0) for a block whose
@@ -221,7 +221,8 @@ AR_API ar_status ar_w4a16_gemm(const void* X, ar_dtype xt, int64_t M, int64_t K,
 
 /* Quantize W DEVICE [N, K] (fp32 or bf16) to packed MXFP4: the codes of
  * ar_qdq_rtn, two per byte.  alpha DEVICE fp32 [N, K/32] clip factors, m =
- * |alpha * max|x_b||, nullable (= 1).  (For block maxima below 2^-125 ar_qdq_rtn
+ * |alpha * max|x_b||, nullable (= 1); they are the caller's own: the tuning
+ * entry points do not tune for this format.  (For block maxima below 2^-125 ar_qdq_rtn
  * takes exponents under -127, which the scale byte cannot hold; here e stays
  * at -127.) */
 AR_API ar_status ar_pack_mxfp4(const void* W, ar_dtype wt, int64_t N, int64_t K, const float* alpha,
@@ -255,8 +256,10 @@ AR_API ar_status ar_swiglu_mxfp4(const void* gate, int64_t ld_gate, const void* 
                           int64_t F, uint8_t* packed, uint8_t* scale, void* stream);
 
 /* MXFP4-weight GEMM on bf16 activations: Y[m, n] = sum_k X[m, k] W[n, k] with
- * W the values of packed [N, K/2] / scale [N, K/32] (exact in bf16) and fp32
- * accumulation.  X DEVICE bf16 [M, K], Y DEVICE [M, N] of dtype yt, row-major. */
+ * W the values of packed [N, K/2] / scale [N, K/32] (exact in bf16; values of
+ * the scale bytes 253 and 254 beyond the fp32 range, which no quantizer here
+ * writes, are infinite) and fp32 accumulation.  X DEVICE bf16 [M, K], Y DEVICE
+ * [M, N] of dtype yt, row-major. */
 AR_API ar_status ar_mxfp4_gemm(const void* X, int64_t M, int64_t K, const uint8_t* packed, const uint8_t* scale,
                         int64_t N, void* Y, ar_dtype yt, void* stream);
 

@@ -11,7 +11,7 @@ using namespace ar::rt;
 namespace {
 
 constexpr int64_t kMaxElems = (int64_t)1 << 34;
-constexpr int64_t kMaxReach = (int64_t)1 << 40;   // last row's distance in elements: more than any memory, and its bytes fit 64 bits
+constexpr int64_t kMaxReach = (int64_t)1 << 40;   // the last row's distance in elements: past any memory
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
@@ -31,7 +31,9 @@ struct Span {
 };
 
 // Outputs overlap no input and no other output: workgroups read what others
-// have not finished with in no fixed order.
+// have not finished with in no fixed order.  (The norm alone could write r_out
+// over x or a bf16 delta, as one workgroup holds a row before it writes any of
+// it; it keeps to the rule of the others.)
 ar_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
     auto meet = [](const Span& a, const Span& b) {
         const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);

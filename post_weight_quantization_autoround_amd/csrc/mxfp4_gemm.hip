@@ -703,10 +703,17 @@ void launch_a4_tile(const MxGemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 // The tile is the smallest that does not need more workgroups than the 256
-// CUs, otherwise the largest: a workgroup's time is that of its K loop, most of
-// it latency, so one round of small tiles beats a part-filled round of large
-// ones, and with several rounds what counts is how often a tile re-reads its
-// operands.  Measured (us, the choice first):
+// CUs: a workgroup's time is that of its K loop, most of it latency, so one
+// round of small tiles beats a part-filled round of large ones.  With several
+// rounds what counts is how often a tile re-reads its operands, so the largest
+// tile follows, with three exceptions: up to 32 rows stay in tiles of 32 rows
+// whatever the number of rounds; 64x128 (bf16 X) and 128x128 (packed X off the
+// tile kernels' alignment) are taken up to two rounds; and for bf16 X the fuller
+// last round decides between 256x256 and 128x256.  The rule counts tiles and not
+// the rows of them that lie past M: with more than 65,536 outputs 33 to 128 rows
+// take 256x256, half of it or more past M (40 x 128256 x 4096 175 us with bf16 X
+// and 81 with packed X, 128 rows 195 and 86, where the weight streams in 48).
+// Measured (us, the choice first):
 //   bf16 X: 16 x 8192 x 28672 32x32 40-43, 32x64 56; 16 x 28672 x 8192 32x128 29,
 //   32x64 34, 64x128 39; 64 x 4096 x 4096 32x32 8.8, 32x64 10, 64x64 14; 130 x
 //   4096 x 11008 64x64 30, 64x128 39; 256 x 11008 x 4096 64x128 in two rounds 36,
@@ -736,7 +743,8 @@ hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream) {
     else if (tiles(a, 128, 256) <= 256) launch_ring<false, 128, 256, 2, 4, 1, 4, 3>(a, stream);
     else {
         // Several rounds: 256x256 is 6% faster a flop, 128x256 (two workgroups a
-        // CU, so at most 128 registers) fills its last round better.
+        // CU, so at most 128 registers, two of them spilled outside the K loop)
+        // fills its last round better.
         const int64_t big = tiles(a, 256, 256), small = tiles(a, 128, 256);
         const double full_big = (double)big / (double)((big + 255) / 256), full_small = (double)small / (double)((small + 255) / 256);
         if (1.06 * full_big >= full_small) launch_ring<false, 256, 256, 2, 4, 1, 2, 3>(a, stream);

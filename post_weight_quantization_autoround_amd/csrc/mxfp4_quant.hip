@@ -212,8 +212,8 @@ __device__ __forceinline__ bool quantize_guarded(const float h[8], float D, uint
 // -------------------------------------------------------------- RMS norm ----
 // r = x + c delta (fp32), h = r / sqrt(mean(r^2) + eps) * w.  A workgroup
 // takes a row and keeps it in registers (8 CH elements a thread), so x and
-// delta are read once (2048 x 8192 with a bf16 delta: 22 us, 4.9 TB/s of what
-// has to move, HBM's rate).  The squares are summed in fp64: the fast path's h
+// delta are read once (2048 x 8192 with a bf16 delta: 22-24 us, 4.6-4.9 TB/s of
+// what has to move, HBM's rate).  The squares are summed in fp64: the fast path's h
 // then differs from the fp64 value by the roundings of 1/rms to fp32 and of
 // two products, 3 * 2^-24 in all (2^-22 + 2 * 2^-24 where 1/rms is subnormal).
 // Where r/rms itself is below 2^-126 the relative error has no such bound: with
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(MxNormArgs a) {
 }
 
 // ---------------------------------------------------------------- SwiGLU ----
-// 4096 x 28672: 103 us, 5.2 TB/s of what has to move: HBM's rate.
+// 4096 x 28672: 91-109 us, 4.9-5.8 TB/s of what has to move: HBM's rate.
 // h = g / (1 + exp(-g)) u.  Fast path: exp(-g) = 2^(-g log2 e) by v_exp_f32
 // and v_rcp_f32.  Its error is that of the exponent's product, |g| 2^-23.7
 // relative for g < 0 (below 2^-17.2 down to g = -87.3), plus a few units of
