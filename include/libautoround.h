@@ -269,6 +269,112 @@ AR_API ar_status ar_mxfp4_gemm_a4(const uint8_t* x_packed, const uint8_t* x_scal
                            const uint8_t* packed, const uint8_t* scale, int64_t N, void* Y, ar_dtype yt,
                            void* stream);
 
+/* The activations of an epilogue, act(a):
+ *   RELU       a for a >= 0, else 0             SILU       a / (1 + exp(-a))
+ *   GELU       a (1 + erf(a / sqrt 2)) / 2
+ *   GELU_TANH  a (1 + tanh(sqrt(2/pi) (a + 0.044715 a^3))) / 2
+ * NaN stays NaN; SILU and both GELUs of -inf are NaN, as their formulas are. */
+typedef enum { AR_ACT_NONE = 0, AR_ACT_RELU = 1, AR_ACT_SILU = 2, AR_ACT_GELU = 3, AR_ACT_GELU_TANH = 4 } ar_act;
+
+/* The products of ar_mxfp4_gemm and ar_mxfp4_gemm_a4 with an epilogue:
+ *   Y[m, n] = residual[m, n] + act(sum_k X[m, k] W[n, k] + bias[n])
+ * in fp32 throughout, rounded once to yt.
+ *  bias      DEVICE [N] of bias_dtype, nullable
+ *  act       ar_act
+ *  residual  DEVICE [M, N] of residual_dtype, rows ld_residual elements apart,
+ *            nullable (its dtype and stride are then not used)
+ *  Y         DEVICE [M, N] of dtype yt, rows ldy elements apart; what lies between
+ *            its rows is not written.  Y may be the residual itself (same pointer,
+ *            dtype and stride); otherwise Y, first to last element, overlaps no input
+ * The other arguments and the common errors are those of the products;
+ * besides, AR_ERR_INVALID_ARG for an unknown act or a stride below N,
+ * AR_ERR_UNSUPPORTED for rows that reach past 2^40 elements or a bias or
+ * residual that is not aligned as its type.  Nothing is allocated;
+ * stream-ordered, no synchronization. */
+AR_API ar_status ar_mxfp4_linear(const void* X, int64_t M, int64_t K, const uint8_t* packed, const uint8_t* scale,
+                          int64_t N, const void* bias, ar_dtype bias_dtype, int32_t act, const void* residual,
+                          ar_dtype residual_dtype, int64_t ld_residual, void* Y, ar_dtype yt, int64_t ldy, void* stream);
+AR_API ar_status ar_mxfp4_linear_a4(const uint8_t* x_packed, const uint8_t* x_scale, int64_t M, int64_t K,
+                             const uint8_t* packed, const uint8_t* scale, int64_t N, const void* bias,
+                             ar_dtype bias_dtype, int32_t act, const void* residual, ar_dtype residual_dtype,
+                             int64_t ld_residual, void* Y, ar_dtype yt, int64_t ldy, void* stream);
+
+/* The same products grouped by expert, W_e and bias_e those of expert e: for
+ * offsets[e] <= p < offsets[e + 1],
+ *   Y[p, n] = act(sum_k X[r(p), k] W_e[n, k] + bias_e[n]),  r(p) = rows[p], or p without rows.
+ *  X        DEVICE bf16 [x_rows, K] (a4: x_packed [x_rows, K/2], x_scale
+ *           [x_rows, K/32])
+ *  rows     DEVICE int32 [M], nullable (x_rows must be M then); an index outside
+ *           [0, x_rows) stands for a row of zeros.  ar_moe_route writes them
+ *  packed   DEVICE uint8 [E, N, K/2], scale DEVICE uint8 [E, N, K/32], bias
+ *           DEVICE [E, N] of bias_dtype, nullable; E at most 1024
+ *  offsets  DEVICE int32 [E + 1], ascending, within [0, M]: any group may be
+ *           empty.  They are read on the device: a call waits for nothing, and one
+ *           captured into a HIP graph follows the offsets of each replay.  Offsets that
+ *           do not ascend or leave [0, M] are cut to it: the rows of Y are then
+ *           undefined, but nothing outside the buffers is read or written
+ *  Y        DEVICE [M, N] of dtype yt; rows outside [offsets[0], offsets[E]) are left
+ *           as they were
+ * M = 0 is an empty problem (AR_OK).  Errors as for the products; besides,
+ * AR_ERR_UNSUPPORTED for E > 1024, M > 2^24, more than 2^34 elements of
+ * packed, or rows with an X of 2^31 bytes or more.  Nothing is allocated;
+ * stream-ordered, no synchronization. */
+AR_API ar_status ar_mxfp4_grouped_gemm(const void* X, int64_t x_rows, int64_t K, const int32_t* rows,
+                                const uint8_t* packed, const uint8_t* scale, int32_t E, int64_t N,
+                                const int32_t* offsets, const void* bias, ar_dtype bias_dtype, int32_t act, void* Y,
+                                ar_dtype yt, int64_t M, void* stream);
+AR_API ar_status ar_mxfp4_grouped_gemm_a4(const uint8_t* x_packed, const uint8_t* x_scale, int64_t x_rows, int64_t K,
+                                   const int32_t* rows, const uint8_t* packed, const uint8_t* scale, int32_t E,
+                                   int64_t N, const int32_t* offsets, const void* bias, ar_dtype bias_dtype,
+                                   int32_t act, void* Y, ar_dtype yt, int64_t M, void* stream);
+
+typedef enum { AR_SCORE_SOFTMAX = 0, AR_SCORE_SIGMOID = 1 } ar_score;
+
+/* The router in front of the grouped products: k of E experts for each of T
+ * tokens, and the T k slots s = t k + j sorted by expert.
+ * With s_e the softmax or the sigmoid of a token's logits, the choice goes by
+ * s_e, or by s_e + bias_e with a bias: the k largest in descending order, ties
+ * to the lowest index, NaN before all.  A score of -inf (logit or bias) is
+ * never chosen: a token with fewer than k others has slots of no expert.
+ *   weight = weight_scale * s_e, or weight_scale * s_e / (sum of the token's
+ *            chosen s) with normalize != 0 (0 where that sum is 0); the softmax runs
+ *            over all E, also with a bias; 0 for slots of no expert.  Computed in 64
+ *            bits, rounded once
+ *  logits   DEVICE [T, E] of dtype lt;  bias DEVICE fp32 [E], nullable
+ *  score    ar_score
+ *  expert   DEVICE int32 [T, k], -1 for no expert;  weight DEVICE fp32 [T, k]
+ *  offsets  DEVICE int32 [E + 1]: expert e has rows [offsets[e], offsets[e + 1]),
+ *           its slots in ascending order
+ *  token    DEVICE int32 [T k]: the token of each row (`rows` of the grouped
+ *           products), -1 from offsets[E] on
+ *  pos      DEVICE int32 [T, k]: the row of each slot, -1 for no expert
+ * T = 0 writes zero offsets (the other pointers may be NULL).  Errors:
+ * AR_ERR_INVALID_ARG for a NULL pointer, T < 0, E < 1, k outside 1..E, an
+ * unknown dtype or score, or an output that overlaps an input or another
+ * output; AR_ERR_UNSUPPORTED for E > 1024, k > 64, T k > 2^24 or a pointer
+ * that is not aligned as its type.  The result depends on nothing but the
+ * inputs.  Nothing is allocated; stream-ordered, no synchronization. */
+AR_API ar_status ar_moe_route(const void* logits, ar_dtype lt, int64_t T, int32_t E, int32_t k, int32_t score,
+                       const float* bias, int32_t normalize, float weight_scale, int32_t* expert, float* weight,
+                       int32_t* offsets, int32_t* token, int32_t* pos, void* stream);
+
+/* The sum behind the grouped products:
+ *   Y[t, n] = residual[t, n] + sum_j weight[t, j] Z[pos[t, j], n]
+ * in fp32, j ascending, the residual last, rounded once to yt.
+ *  Z         DEVICE [P, N] of dtype zt
+ *  pos       DEVICE int32 [T, k], weight DEVICE fp32 [T, k] (ar_moe_route's); a
+ *            pos outside [0, P) adds nothing, whatever its weight
+ *  residual  DEVICE [T, N] of residual_dtype, nullable; Y DEVICE [T, N] of dtype
+ *            yt.  Y may be the residual itself (same pointer and dtype)
+ * T = 0 is an empty problem.  Errors: AR_ERR_INVALID_ARG for a NULL pointer,
+ * P < 0, N < 1, T < 0, k < 1, an unknown dtype or an output that overlaps an
+ * input; AR_ERR_UNSUPPORTED for k > 64, T k > 2^24, more than 2^34 elements or
+ * a pointer that is not aligned as its type.  Nothing is allocated;
+ * stream-ordered, no synchronization. */
+AR_API ar_status ar_moe_combine(const void* Z, ar_dtype zt, int64_t P, int64_t N, const int32_t* pos, const float* weight,
+                         int64_t T, int32_t k, const void* residual, ar_dtype residual_dtype, void* Y, ar_dtype yt,
+                         void* stream);
+
 /* One evaluation of the tuning objective and its straight-through gradients
  * (blog sec. 3 algorithm flow, steps 2-4) on the samples ids[0..B-1] of the
  * pool X_pool DEVICE [S, T, K] (dtype xt; M = B*T rows):

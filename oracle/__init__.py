@@ -42,6 +42,7 @@ from .autoround_ref import (  # noqa: F401
 )
 from .bruteforce import bruteforce_min_loss, bruteforce_block_min_loss  # noqa: F401
 from . import decoder_ref  # noqa: F401
+from . import moe_ref  # noqa: F401
 from . import mxfp4_ref  # noqa: F401
 from .block_ref import (  # noqa: F401
     LINEARS,

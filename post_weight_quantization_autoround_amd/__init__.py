@@ -103,6 +103,12 @@ def _load() -> ctypes.CDLL:
         "ar_swiglu_mxfp4": (st, [P, I64, P, I64, I64, I64, P, P, P]),
         "ar_mxfp4_gemm": (st, [P, I64, I64, P, P, I64, P, st, P]),
         "ar_mxfp4_gemm_a4": (st, [P, P, I64, I64, P, P, I64, P, st, P]),
+        "ar_mxfp4_linear": (st, [P, I64, I64, P, P, I64, P, st, I32, P, st, I64, P, st, I64, P]),
+        "ar_mxfp4_linear_a4": (st, [P, P, I64, I64, P, P, I64, P, st, I32, P, st, I64, P, st, I64, P]),
+        "ar_mxfp4_grouped_gemm": (st, [P, I64, I64, P, P, P, I32, I64, P, P, st, I32, P, st, I64, P]),
+        "ar_mxfp4_grouped_gemm_a4": (st, [P, P, I64, I64, P, P, P, I32, I64, P, P, st, I32, P, st, I64, P]),
+        "ar_moe_route": (st, [P, st, I64, I32, I32, I32, P, I32, F, P, P, P, P, P, P]),
+        "ar_moe_combine": (st, [P, st, I64, I64, P, P, I64, I32, P, st, P, st, P]),
         "ar_layer_grads": (st, [P, st, I64, I64, P, st, I64, I64, ctypes.POINTER(ctypes.c_int32), I32, qc, st,
                                 P, P, P, ctypes.POINTER(D), P, P, P, P, P]),
         "ar_tune_layer": (st, [P, st, I64, I64, P, st, I64, I64, qc, op, P, P, P,
@@ -410,6 +416,169 @@ def mxfp4_gemm_a4(x_packed: torch.Tensor, x_scale: torch.Tensor, packed: torch.T
     ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
     out = _mx_y(out, out_dtype, M, N, x_packed, dev)
     _check(lib.ar_mxfp4_gemm_a4(px, pxs, M, K, pp, ps, N, out.data_ptr(), _dtype_code(out), _mx_stream(dev)))
+    return out
+
+
+# ------------------------- packed MXFP4: epilogues, mixture of experts
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
+_I32 = (torch.int32,)
+
+
+def _named(table, name, what):
+    try:
+        return table[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what} must be one of {', '.join(table)}, got {name!r}") from None
+
+
+def _row_stride(t):
+    # the stride of a lone row means nothing
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _mx_linear(call, M, K, x, packed, scale, bias, act, residual, out_dtype, out, like, dev):
+    pp = _mx_in(packed, "packed", _U8, dev)
+    N = packed.shape[0]
+    if 2 * packed.shape[1] != K:
+        raise ValueError(f"X has {K} columns, packed holds {2 * packed.shape[1]}")
+    ps = _mx_in(scale, "scale", _U8, dev, (N, K // 32))
+    code = _named(ACTIVATIONS, act, "act")
+    pb, bt = (None, 0) if bias is None else (_mx_in(bias, "bias", _F32_BF16, dev, (N,)), _dtype_code(bias))
+    pr, rt, ldr = None, 0, 0
+    if residual is not None:
+        pr = _mx_in(residual, "residual", _F32_BF16, dev, (M, N), True)
+        rt, ldr = _dtype_code(residual), _row_stride(residual)
+    if out is None:
+        out = like.new_empty((M, N), dtype=out_dtype)
+        py, ldy = out.data_ptr(), N
+    else:
+        py = _mx_in(out, "out", (out_dtype,), dev, (M, N), True)
+        ldy = _row_stride(out)
+    _check(call(*x, M, K, pp, ps, N, pb, bt, code, pr, rt, ldr, py, _dtype_code(out), ldy, _mx_stream(dev)))
+    return out
+
+
+def mxfp4_linear(X: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor | None = None,
+                 act: str = "none", residual: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                 out: torch.Tensor | None = None):
+    """Y = residual + act(X W^T + bias), mxfp4_gemm with an epilogue: X bf16
+    [M, K], packed uint8 [N, K/2], scale uint8 [N, K/32], bias [N] and residual
+    [M, N] fp32 or bf16, act "none", "relu", "silu", "gelu" (erf) or "gelu_tanh".
+    residual and out may have strided rows; out may be the residual itself."""
+    dev = _mx_dev()
+    px = _mx_in(X, "X", _BF16, dev)
+    M, K = X.shape
+    return _mx_linear(lib.ar_mxfp4_linear, M, K, (px,), packed, scale, bias, act, residual, out_dtype, out, X, dev)
+
+
+def mxfp4_linear_a4(x_packed: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
+                    bias: torch.Tensor | None = None, act: str = "none", residual: torch.Tensor | None = None,
+                    out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
+    """mxfp4_linear with activations in packed MXFP4 too (x_packed uint8
+    [M, K/2], x_scale uint8 [M, K/32])."""
+    dev = _mx_dev()
+    px = _mx_in(x_packed, "x_packed", _U8, dev)
+    M, K = x_packed.shape[0], 2 * x_packed.shape[1]
+    pxs = _mx_in(x_scale, "x_scale", _U8, dev, (M, K // 32))
+    return _mx_linear(lib.ar_mxfp4_linear_a4, M, K, (px, pxs), packed, scale, bias, act, residual, out_dtype, out,
+                      x_packed, dev)
+
+
+def _mx_grouped(call, x_rows, K, x, packed, scale, offsets, rows, bias, act, out_dtype, out, like, dev):
+    if not isinstance(packed, torch.Tensor) or packed.dim() != 3:
+        raise ValueError("packed must be a tensor [E, N, K/2]")
+    E, N, half = packed.shape
+    pp = _mx_in(packed, "packed", _U8, dev, packed.shape)
+    if 2 * half != K:
+        raise ValueError(f"X has {K} columns, packed holds {2 * half}")
+    ps = _mx_in(scale, "scale", _U8, dev, (E, N, K // 32))
+    po = _mx_in(offsets, "offsets", _I32, dev, (E + 1,))
+    M, pr = x_rows, None
+    if rows is not None:
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            raise ValueError("rows must be a tensor of one dimension")
+        M = rows.shape[0]
+        pr = _mx_in(rows, "rows", _I32, dev, (M,))
+    code = _named(ACTIVATIONS, act, "act")
+    pb, bt = (None, 0) if bias is None else (_mx_in(bias, "bias", _F32_BF16, dev, (E, N)), _dtype_code(bias))
+    out = _mx_y(out, out_dtype, M, N, like, dev)
+    _check(call(*x, x_rows, K, pr, pp, ps, E, N, po, pb, bt, code, out.data_ptr(), _dtype_code(out), M,
+                _mx_stream(dev)))
+    return out
+
+
+def mxfp4_grouped_gemm(X: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, offsets: torch.Tensor,
+                       rows: torch.Tensor | None = None, bias: torch.Tensor | None = None, act: str = "none",
+                       out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
+    """Products grouped by expert: Y[p] = act(X[rows[p]] W_e^T + bias[e]) for
+    offsets[e] <= p < offsets[e + 1] (X[p] without rows).  X bf16 [R, K], packed
+    uint8 [E, N, K/2], scale uint8 [E, N, K/32], offsets int32 [E + 1] and rows
+    int32 [M] as moe_route returns them (read on the GPU), bias [E, N] fp32 or
+    bf16.  Returns Y [M, N]; rows outside [offsets[0], offsets[E]) are not
+    written (uninitialised without `out`)."""
+    dev = _mx_dev()
+    px = _mx_in(X, "X", _BF16, dev)
+    return _mx_grouped(lib.ar_mxfp4_grouped_gemm, X.shape[0], X.shape[1], (px,), packed, scale, offsets, rows, bias, act,
+                       out_dtype, out, X, dev)
+
+
+def mxfp4_grouped_gemm_a4(x_packed: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
+                          offsets: torch.Tensor, rows: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                          act: str = "none", out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
+    """mxfp4_grouped_gemm with activations in packed MXFP4 too (x_packed uint8
+    [R, K/2], x_scale uint8 [R, K/32])."""
+    dev = _mx_dev()
+    px = _mx_in(x_packed, "x_packed", _U8, dev)
+    R, K = x_packed.shape[0], 2 * x_packed.shape[1]
+    pxs = _mx_in(x_scale, "x_scale", _U8, dev, (R, K // 32))
+    return _mx_grouped(lib.ar_mxfp4_grouped_gemm_a4, R, K, (px, pxs), packed, scale, offsets, rows, bias, act, out_dtype,
+                       out, x_packed, dev)
+
+
+def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", normalize: bool = True,
+              bias: torch.Tensor | None = None, weight_scale: float = 1.0):
+    """The k experts of each token by softmax or sigmoid scores (by score +
+    bias [E] with a bias), their weights, and the slots t k + j sorted by
+    expert.  logits fp32 or bf16 [T, E]; a logit of -inf is never chosen.
+    Returns (expert int32 [T, k], -1 for none; weight fp32 [T, k], divided by the
+    token's sum if `normalize`, times weight_scale; offsets int32 [E + 1]; token
+    int32 [T k], the token of each row, -1 behind the last; pos int32 [T, k], the
+    row of each slot)."""
+    dev = _mx_dev()
+    pl = _mx_in(logits, "logits", _F32_BF16, dev)
+    T, E = logits.shape
+    pb = None if bias is None else _mx_in(bias, "bias", _F32, dev, (E,))
+    how = _named(SCORES, score, "score")
+    k = int(k)
+    n = max(k, 0)
+    expert, pos = (logits.new_empty((T, n), dtype=torch.int32) for _ in range(2))
+    weight = logits.new_empty((T, n), dtype=torch.float32)
+    offsets = logits.new_empty(E + 1, dtype=torch.int32)
+    token = logits.new_empty(T * n, dtype=torch.int32)
+    _check(lib.ar_moe_route(pl, _dtype_code(logits), T, E, k, how, pb, int(normalize), weight_scale, expert.data_ptr(),
+                            weight.data_ptr(), offsets.data_ptr(), token.data_ptr(), pos.data_ptr(), _mx_stream(dev)))
+    return expert, weight, offsets, token, pos
+
+
+def moe_combine(Z: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
+    """Y[t] = residual[t] + sum_j weight[t, j] Z[pos[t, j]]; Z fp32 or bf16
+    [P, N], pos int32 and weight fp32 [T, k] as moe_route returns them (a pos
+    outside [0, P) adds nothing), residual fp32 or bf16 [T, N].  out may be the
+    residual itself."""
+    dev = _mx_dev()
+    pz = _mx_in(Z, "Z", _F32_BF16, dev)
+    pp = _mx_in(pos, "pos", _I32, dev)
+    T, k = pos.shape
+    pw = _mx_in(weight, "weight", _F32, dev, (T, k))
+    P, N = Z.shape
+    pr, rt = None, 0
+    if residual is not None:
+        pr, rt = _mx_in(residual, "residual", _F32_BF16, dev, (T, N)), _dtype_code(residual)
+    out = _mx_y(out, out_dtype, T, N, Z, dev)
+    _check(lib.ar_moe_combine(pz, _dtype_code(Z), P, N, pp, pw, T, k, pr, rt, out.data_ptr(), _dtype_code(out),
+                              _mx_stream(dev)))
     return out
 
 

@@ -59,4 +59,32 @@ struct MxGemmArgs {
 hipError_t launch_mx_gemm_a16(const MxGemmArgs& a, hipStream_t stream);
 hipError_t launch_mx_gemm_a4(const MxGemmArgs& a, hipStream_t stream);
 
+enum { kMxNone = 0, kMxRelu = 1, kMxSilu = 2, kMxGelu = 3, kMxGeluTanh = 4 };   // ar_act
+
+// Y = res + act(X W^T + bias)
+struct MxLinearArgs : MxGemmArgs {
+    const void* bias; bool bias_bf16;          // [N], nullable
+    int act;
+    const void* res; bool res_bf16; int64_t ldr;   // rows ldr apart, nullable; may be y with the same type and stride
+    int64_t ldy;                               // rows of y
+    bool wide;                                 // four neighbouring columns of y, res and bias lie in one aligned piece
+};
+hipError_t launch_mx_linear_a16(const MxLinearArgs& a, hipStream_t stream);
+hipError_t launch_mx_linear_a4(const MxLinearArgs& a, hipStream_t stream);
+
+// Rows [offsets[e], offsets[e + 1]) of Y by expert e: wp [E, N, K/2], ws
+// [E, N, K/32], bias [E, N], M rows of Y, no residual.
+struct MxGroupArgs : MxLinearArgs {
+    const int32_t* offsets;                    // [E + 1]
+    const int32_t* rows;                       // [M] row of X, nullable (= the row of Y)
+    int64_t x_rows;
+    int32_t E;                                 // at most kMxMaxExperts
+};
+constexpr int32_t kMxMaxExperts = 1024;
+constexpr int64_t kMxMaxGroupRows = 1 << 24;   // the experts' tile rows, were each given all rows, count up within 32 bits
+// Threads of the largest launch that the group sizes may need; the kernels' grids hold below 2^32.
+int64_t mx_grouped_threads(const MxGroupArgs& a, bool a4);
+hipError_t launch_mx_grouped_a16(const MxGroupArgs& a, hipStream_t stream);
+hipError_t launch_mx_grouped_a4(const MxGroupArgs& a, hipStream_t stream);
+
 }  // namespace ar

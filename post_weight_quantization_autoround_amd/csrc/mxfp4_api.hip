@@ -1,72 +1,107 @@
 // C ABI of the packed-MXFP4 operators: host checks, then one launch each.
 // Nothing is allocated.
-#include <initializer_list>
-
-#include "mxfp4.h"
-#include "tuner.h"
+#include "mxfp4_checks.h"
 
 using namespace ar;
 using namespace ar::rt;
 
 namespace {
 
-constexpr int64_t kMaxElems = (int64_t)1 << 34;
-constexpr int64_t kMaxReach = (int64_t)1 << 40;   // the last row's distance in elements: past any memory
+int64_t size_of(ar_dtype d) { return d == AR_BF16 ? 2 : 4; }
 
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// rows >= 0, cols > 0, a multiple of 32, rows * cols within range
-ar_status check_shape(const char* rn, int64_t rows, const char* cn, int64_t cols) {
-    if (rows < 0 || cols <= 0) return fail(AR_ERR_INVALID_ARG, "need %s >= 0 and %s > 0", rn, cn);
-    if (cols % 32 != 0)
-        return fail(AR_ERR_INVALID_ARG, "%s must be a multiple of 32 (the MXFP4 block), got %lld", cn, (long long)cols);
-    if (cols >= ((int64_t)1 << 30)) return fail(AR_ERR_UNSUPPORTED, "%s must be below 2^30", cn);
-    if (rows > kMaxElems / cols) return fail(AR_ERR_UNSUPPORTED, "problem too large");
+// Bias, activation, residual and output of a product; bias [experts, N].
+ar_status check_epilogue(int64_t M, int64_t N, const void* bias, ar_dtype bias_dtype, int32_t act, const void* residual,
+                         ar_dtype residual_dtype, int64_t ld_residual, int64_t ldy) {
+    if (act < AR_ACT_NONE || act > AR_ACT_GELU_TANH) return fail(AR_ERR_INVALID_ARG, "unknown activation %d", act);
+    if (bias && !dtype_ok(bias_dtype)) return fail(AR_ERR_INVALID_ARG, "unknown bias dtype");
+    if (residual && !dtype_ok(residual_dtype)) return fail(AR_ERR_INVALID_ARG, "unknown residual dtype");
+    if (ldy < N || (residual && ld_residual < N))
+        return fail(AR_ERR_INVALID_ARG, "ldy and ld_residual must be at least N");
+    if (M > 1 && (ldy > kMaxReach / (M - 1) || (residual && ld_residual > kMaxReach / (M - 1))))
+        return fail(AR_ERR_UNSUPPORTED, "a row stride reaches past 2^40 elements");
+    if (bias && !aligned(bias, size_of(bias_dtype))) return fail(AR_ERR_UNSUPPORTED, "bias must be aligned as its type");
+    if (residual && !aligned(residual, size_of(residual_dtype)))
+        return fail(AR_ERR_UNSUPPORTED, "residual must be aligned as its type");
     return AR_OK;
 }
 
-struct Span {
-    const void* p;   // nullable: not there
-    int64_t bytes;
-};
-
-// Outputs overlap no input and no other output: workgroups read what others
-// have not finished with in no fixed order.  (The norm alone could write r_out
-// over x or a bf16 delta, as one workgroup holds a row before it writes any of
-// it; it keeps to the rule of the others.)
-ar_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-    auto meet = [](const Span& a, const Span& b) {
-        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-        return a.p && b.p && (x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes);
-    };
-    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
-        for (const Span& i : ins)
-            if (meet(*o, i)) return fail(AR_ERR_INVALID_ARG, "an output overlaps an input");
-        for (const Span* q = outs.begin(); q != o; ++q)
-            if (meet(*o, *q)) return fail(AR_ERR_INVALID_ARG, "two outputs overlap");
-    }
-    return AR_OK;
+MxLinearArgs linear_args(int64_t M, int64_t N, int64_t K, const uint8_t* packed, const uint8_t* scale, const void* bias,
+                         ar_dtype bias_dtype, int32_t act, const void* residual, ar_dtype residual_dtype,
+                         int64_t ld_residual, void* Y, ar_dtype yt, int64_t ldy) {
+    MxLinearArgs a{};
+    a.wp = packed; a.ws = scale; a.M = M; a.N = N; a.K = K; a.y = Y; a.y_bf16 = (yt == AR_BF16);
+    a.bias = bias; a.bias_bf16 = (bias_dtype == AR_BF16); a.act = act;
+    a.res = residual; a.res_bf16 = (residual_dtype == AR_BF16); a.ldr = residual ? ld_residual : 0; a.ldy = ldy;
+    a.wide = N % 4 == 0 && ldy % 4 == 0 && a.ldr % 4 == 0 && aligned(Y, 4 * size_of(yt)) &&
+             (!bias || aligned(bias, 4 * size_of(bias_dtype))) &&
+             (!residual || aligned(residual, 4 * size_of(residual_dtype)));
+    return a;
 }
 
-ar_status launched(hipError_t e, const char* what) {
-    if (e != hipSuccess) return fail(AR_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
-    return AR_OK;
-}
-
-ar_status check_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* packed, const uint8_t* scale, ar_dtype yt) {
-    ar_status st = check_shape("M", M, "K", K);
+// X as spans: the values, and the scale bytes of packed X
+ar_status linear(bool a4, const void* X, const uint8_t* x_scale, int64_t M, int64_t K, const uint8_t* packed,
+                 const uint8_t* scale, int64_t N, const void* bias, ar_dtype bias_dtype, int32_t act,
+                 const void* residual, ar_dtype residual_dtype, int64_t ld_residual, void* Y, ar_dtype yt, int64_t ldy,
+                 void* stream) {
+    ar_status st = check_gemm(M, N, K, packed, scale, yt);
     if (st != AR_OK) return st;
-    if (N <= 0) return fail(AR_ERR_INVALID_ARG, "need N > 0");
-    st = check_shape("N", N, "K", K);
+    st = check_epilogue(M, N, bias, bias_dtype, act, residual, residual_dtype, ld_residual, ldy);
     if (st != AR_OK) return st;
-    // at most 2^34 / 32 rows on either side: the product of the two cannot overflow
-    // (2^37 outputs in tiles of at least 2^15 by 512 threads: fewer than 2^32 threads)
-    if (M * N > (int64_t)1 << 37) return fail(AR_ERR_UNSUPPORTED, "Y may hold at most 2^37 elements");
-    if (K >= kMxGemmMaxK) return fail(AR_ERR_UNSUPPORTED, "the products need K below %lld", (long long)kMxGemmMaxK);
-    if (!packed || !scale) return fail(AR_ERR_INVALID_ARG, "packed and scale must be non-NULL");
-    if (!dtype_ok(yt)) return fail(AR_ERR_INVALID_ARG, "unknown output dtype");
-    if (!aligned(packed, 16)) return fail(AR_ERR_UNSUPPORTED, "packed must be 16-byte aligned");
-    return AR_OK;
+    if (M == 0) return AR_OK;
+    if (!X || (a4 && !x_scale) || !Y) return fail(AR_ERR_INVALID_ARG, "X and Y must be non-NULL when M > 0");
+    if (!aligned(X, 16) || !aligned(Y, size_of(yt)))
+        return fail(AR_ERR_UNSUPPORTED, "X must be 16-byte aligned and Y as its type");
+    // each element of Y is written by the thread that read the same element of the residual before
+    const bool in_place = residual == Y && residual_dtype == yt && ld_residual == ldy;
+    const Span x = {X, a4 ? M * K / 2 : 2 * M * K}, xs = {x_scale, M * K / 32};
+    const Span res = {in_place ? nullptr : residual, ((M - 1) * ld_residual + N) * size_of(residual_dtype)};
+    st = check_apart({{Y, ((M - 1) * ldy + N) * size_of(yt)}},
+                     {x, xs, {packed, N * K / 2}, {scale, N * K / 32}, {bias, N * size_of(bias_dtype)}, res});
+    if (st != AR_OK) return st;
+    MxLinearArgs a = linear_args(M, N, K, packed, scale, bias, bias_dtype, act, residual, residual_dtype, ld_residual, Y,
+                                 yt, ldy);
+    if (a4) { a.xp = static_cast<const uint8_t*>(X); a.xs = x_scale; }
+    else a.x = static_cast<const uint16_t*>(X);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return launched(a4 ? launch_mx_linear_a4(a, s) : launch_mx_linear_a16(a, s), "MXFP4 linear");
+}
+
+ar_status grouped(bool a4, const void* X, const uint8_t* x_scale, int64_t x_rows, int64_t K, const int32_t* rows,
+                  const uint8_t* packed, const uint8_t* scale, int32_t E, int64_t N, const int32_t* offsets,
+                  const void* bias, ar_dtype bias_dtype, int32_t act, void* Y, ar_dtype yt, int64_t M, void* stream) {
+    if (E <= 0) return fail(AR_ERR_INVALID_ARG, "need E > 0");
+    if (E > kMxMaxExperts) return fail(AR_ERR_UNSUPPORTED, "at most %d experts, got %d", kMxMaxExperts, E);
+    ar_status st = check_gemm(M, N, K, packed, scale, yt);
+    if (st != AR_OK) return st;
+    if (N > kMaxElems / K / E) return fail(AR_ERR_UNSUPPORTED, "problem too large");
+    st = check_shape("x_rows", x_rows, "K", K);
+    if (st != AR_OK) return st;
+    st = check_epilogue(M, N, bias, bias_dtype, act, nullptr, yt, 0, N);
+    if (st != AR_OK) return st;
+    if (M > kMxMaxGroupRows) return fail(AR_ERR_UNSUPPORTED, "at most %lld rows", (long long)kMxMaxGroupRows);
+    if (!rows && x_rows != M) return fail(AR_ERR_INVALID_ARG, "without rows, X must have the M rows of Y");
+    const int64_t x_bytes = a4 ? x_rows * K / 2 : 2 * x_rows * K;
+    if (rows && x_bytes >= (int64_t)1 << 31) return fail(AR_ERR_UNSUPPORTED, "X of gathered rows must be below 2^31 bytes");
+    if (M == 0) return AR_OK;
+    if (!offsets) return fail(AR_ERR_INVALID_ARG, "offsets must be non-NULL");
+    if (!Y || (x_rows > 0 && (!X || (a4 && !x_scale))))
+        return fail(AR_ERR_INVALID_ARG, "X and Y must be non-NULL when M > 0");
+    if (!aligned(X, 16) || !aligned(Y, size_of(yt)))
+        return fail(AR_ERR_UNSUPPORTED, "X must be 16-byte aligned and Y as its type");
+    if (!aligned(offsets, 4) || !aligned(rows, 4)) return fail(AR_ERR_UNSUPPORTED, "offsets and rows must be 4-byte aligned");
+    const int64_t w = (int64_t)E * N * K;
+    st = check_apart({{Y, M * N * size_of(yt)}},
+                     {{X, x_bytes}, {x_scale, x_rows * K / 32}, {rows, 4 * M}, {offsets, 4 * ((int64_t)E + 1)},
+                      {packed, w / 2}, {scale, w / 32}, {bias, E * N * size_of(bias_dtype)}});
+    if (st != AR_OK) return st;
+    MxGroupArgs a{};
+    static_cast<MxLinearArgs&>(a) = linear_args(M, N, K, packed, scale, bias, bias_dtype, act, nullptr, yt, 0, Y, yt, N);
+    if (a4) { a.xp = static_cast<const uint8_t*>(X); a.xs = x_scale; }
+    else a.x = static_cast<const uint16_t*>(X);
+    a.offsets = offsets; a.rows = rows; a.x_rows = x_rows; a.E = E;
+    if (mx_grouped_threads(a, a4) >= (int64_t)1 << 32) return fail(AR_ERR_UNSUPPORTED, "problem too large");
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return launched(a4 ? launch_mx_grouped_a4(a, s) : launch_mx_grouped_a16(a, s), "MXFP4 grouped GEMM");
 }
 
 }  // namespace
@@ -184,6 +219,37 @@ ar_status ar_mxfp4_gemm_a4(const uint8_t* x_packed, const uint8_t* x_scale, int6
     a.xp = x_packed; a.xs = x_scale;
     a.wp = packed; a.ws = scale; a.M = M; a.N = N; a.K = K; a.y = Y; a.y_bf16 = (yt == AR_BF16);
     return launched(launch_mx_gemm_a4(a, static_cast<hipStream_t>(stream)), "MXFP4 GEMM");
+}
+
+
+ar_status ar_mxfp4_linear(const void* X, int64_t M, int64_t K, const uint8_t* packed, const uint8_t* scale, int64_t N,
+                          const void* bias, ar_dtype bias_dtype, int32_t act, const void* residual,
+                          ar_dtype residual_dtype, int64_t ld_residual, void* Y, ar_dtype yt, int64_t ldy, void* stream) {
+    return linear(false, X, nullptr, M, K, packed, scale, N, bias, bias_dtype, act, residual, residual_dtype, ld_residual,
+                  Y, yt, ldy, stream);
+}
+
+ar_status ar_mxfp4_linear_a4(const uint8_t* x_packed, const uint8_t* x_scale, int64_t M, int64_t K, const uint8_t* packed,
+                             const uint8_t* scale, int64_t N, const void* bias, ar_dtype bias_dtype, int32_t act,
+                             const void* residual, ar_dtype residual_dtype, int64_t ld_residual, void* Y, ar_dtype yt,
+                             int64_t ldy, void* stream) {
+    return linear(true, x_packed, x_scale, M, K, packed, scale, N, bias, bias_dtype, act, residual, residual_dtype,
+                  ld_residual, Y, yt, ldy, stream);
+}
+
+ar_status ar_mxfp4_grouped_gemm(const void* X, int64_t x_rows, int64_t K, const int32_t* rows, const uint8_t* packed,
+                                const uint8_t* scale, int32_t E, int64_t N, const int32_t* offsets, const void* bias,
+                                ar_dtype bias_dtype, int32_t act, void* Y, ar_dtype yt, int64_t M, void* stream) {
+    return grouped(false, X, nullptr, x_rows, K, rows, packed, scale, E, N, offsets, bias, bias_dtype, act, Y, yt, M,
+                   stream);
+}
+
+ar_status ar_mxfp4_grouped_gemm_a4(const uint8_t* x_packed, const uint8_t* x_scale, int64_t x_rows, int64_t K,
+                                   const int32_t* rows, const uint8_t* packed, const uint8_t* scale, int32_t E, int64_t N,
+                                   const int32_t* offsets, const void* bias, ar_dtype bias_dtype, int32_t act, void* Y,
+                                   ar_dtype yt, int64_t M, void* stream) {
+    return grouped(true, x_packed, x_scale, x_rows, K, rows, packed, scale, E, N, offsets, bias, bias_dtype, act, Y, yt, M,
+                   stream);
 }
 
 }  // extern "C"
