@@ -316,9 +316,9 @@ AR_API ar_status ar_mxfp4_linear_a4(const uint8_t* x_packed, const uint8_t* x_sc
  *  Y        DEVICE [M, N] of dtype yt; rows outside [offsets[0], offsets[E]) are left
  *           as they were
  * M = 0 is an empty problem (AR_OK).  Errors as for the products; besides,
- * AR_ERR_UNSUPPORTED for E > 1024, M > 2^24, more than 2^34 elements of
- * packed, or rows with an X of 2^31 bytes or more.  Nothing is allocated;
- * stream-ordered, no synchronization. */
+ * AR_ERR_UNSUPPORTED for E > 1024, M > 2^24, (M / 32 + E) (N / 64 + 1) > 2^23,
+ * more than 2^34 elements of packed, or rows with an X of 2^31 bytes or more.
+ * Nothing is allocated; stream-ordered, no synchronization. */
 AR_API ar_status ar_mxfp4_grouped_gemm(const void* X, int64_t x_rows, int64_t K, const int32_t* rows,
                                 const uint8_t* packed, const uint8_t* scale, int32_t E, int64_t N,
                                 const int32_t* offsets, const void* bias, ar_dtype bias_dtype, int32_t act, void* Y,

@@ -82,8 +82,6 @@ struct MxGroupArgs : MxLinearArgs {
 };
 constexpr int32_t kMxMaxExperts = 1024;
 constexpr int64_t kMxMaxGroupRows = 1 << 24;   // the experts' tile rows, were each given all rows, count up within 32 bits
-// Threads of the largest launch that the group sizes may need; the kernels' grids hold below 2^32.
-int64_t mx_grouped_threads(const MxGroupArgs& a, bool a4);
 hipError_t launch_mx_grouped_a16(const MxGroupArgs& a, hipStream_t stream);
 hipError_t launch_mx_grouped_a4(const MxGroupArgs& a, hipStream_t stream);
 

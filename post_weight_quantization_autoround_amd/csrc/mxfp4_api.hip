@@ -78,6 +78,8 @@ ar_status grouped(bool a4, const void* X, const uint8_t* x_scale, int64_t x_rows
     if (st != AR_OK) return st;
     st = check_epilogue(M, N, bias, bias_dtype, act, nullptr, yt, 0, N);
     if (st != AR_OK) return st;
+    // tiles of at least 32x64 outputs by 256 threads, one more tile row an expert: fewer than 2^32 threads
+    if ((M / 32 + E) * (N / 64 + 1) > (int64_t)1 << 23) return fail(AR_ERR_UNSUPPORTED, "problem too large");
     if (M > kMxMaxGroupRows) return fail(AR_ERR_UNSUPPORTED, "at most %lld rows", (long long)kMxMaxGroupRows);
     if (!rows && x_rows != M) return fail(AR_ERR_INVALID_ARG, "without rows, X must have the M rows of Y");
     const int64_t x_bytes = a4 ? x_rows * K / 2 : 2 * x_rows * K;
@@ -99,7 +101,6 @@ ar_status grouped(bool a4, const void* X, const uint8_t* x_scale, int64_t x_rows
     if (a4) { a.xp = static_cast<const uint8_t*>(X); a.xs = x_scale; }
     else a.x = static_cast<const uint16_t*>(X);
     a.offsets = offsets; a.rows = rows; a.x_rows = x_rows; a.E = E;
-    if (mx_grouped_threads(a, a4) >= (int64_t)1 << 32) return fail(AR_ERR_UNSUPPORTED, "problem too large");
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return launched(a4 ? launch_mx_grouped_a4(a, s) : launch_mx_grouped_a16(a, s), "MXFP4 grouped GEMM");
 }

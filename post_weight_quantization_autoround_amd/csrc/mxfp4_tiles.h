@@ -98,31 +98,33 @@ __device__ __forceinline__ float mx_gelu(float v) {
     return v < 0.0f ? (v * h) * q : v * (1.0f - q * h);
 }
 
-template <bool BF16>
-__device__ __forceinline__ f32x4 mx_activate(f32x4 v, int act) {
-    if (act == kMxRelu) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = v[k] < 0.0f ? 0.0f : v[k];   // NaN stays
-    } else if (act == kMxSilu) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = mx_gate<BF16>(v[k], v[k]);
-    } else if (act == kMxGeluTanh) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = mx_gate<BF16>(v[k], v[k] * (1.5957691216f + 0.0713548163f * (v[k] * v[k])));
-    } else if (act == kMxGelu) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = mx_gelu<BF16>(v[k]);
-    }
-    return v;
+template <bool BF16, int ACT>
+__device__ __forceinline__ float mx_act(float v) {
+    if constexpr (ACT == kMxRelu) return v < 0.0f ? 0.0f : v;   // NaN stays
+    else if constexpr (ACT == kMxSilu) return mx_gate<BF16>(v, v);
+    else if constexpr (ACT == kMxGeluTanh) return mx_gate<BF16>(v, v * (1.5957691216f + 0.0713548163f * (v * v)));
+    else if constexpr (ACT == kMxGelu) return mx_gelu<BF16>(v);
+    else return v;
 }
 
-// Four neighbouring columns of a row: `wide` (N and the row strides multiples
-// of four, addresses aligned to four elements) in one access each, else one
-// by one up to column N.
+// f(std::integral_constant<int, act>{}): one branch ahead of a loop that has one activation's code.
+template <class F>
+__device__ __forceinline__ void mx_with_act(int act, F f) {
+    if (act == kMxNone) f(std::integral_constant<int, kMxNone>{});
+    else if (act == kMxRelu) f(std::integral_constant<int, kMxRelu>{});
+    else if (act == kMxSilu) f(std::integral_constant<int, kMxSilu>{});
+    else if (act == kMxGelu) f(std::integral_constant<int, kMxGelu>{});
+    else f(std::integral_constant<int, kMxGeluTanh>{});
+}
+
+// Four neighbouring columns of a row: WIDE (N and the row strides multiples of
+// four, addresses aligned to four elements) in one access, else one by one up
+// to column N.
+template <bool WIDE>
 struct MxFour {
     u32x4 raw;
-    __device__ __forceinline__ void load(const void* p, bool bf16, int64_t at, int64_t left, bool wide) {
-        if (wide) {
+    __device__ __forceinline__ void load(const void* p, bool bf16, int64_t at, int64_t left) {
+        if constexpr (WIDE) {
             if (bf16) {
                 const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
                 raw[0] = v.x;
@@ -138,35 +140,27 @@ struct MxFour {
                                   : static_cast<const uint32_t*>(p)[at + k];
         }
     }
-    __device__ __forceinline__ f32x4 get(bool bf16, bool wide) const {
+    __device__ __forceinline__ f32x4 get(bool bf16) const {
         f32x4 v;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const uint32_t both = raw[k >> 1];   // of the packed form
-            const uint32_t bits = !bf16 ? raw[k] : !wide ? raw[k] << 16 : k & 1 ? both & 0xFFFF0000u : both << 16;
+            const uint32_t bits = !bf16 ? raw[k] : !WIDE ? raw[k] << 16 : k & 1 ? both & 0xFFFF0000u : both << 16;
             v[k] = __uint_as_float(bits);
         }
         return v;
     }
 };
 
-// The epilogue's inputs of four columns, loaded ahead of the sums.
-template <class Args>
-struct MxAhead {
-    MxFour b, r;
-    __device__ __forceinline__ void load(const Args& a, int64_t brow, int64_t m, int64_t n) {
-        if (a.bias) b.load(a.bias, a.bias_bf16, brow + n, a.N - n, a.wide);
-        if (a.res) r.load(a.res, a.res_bf16, m * a.ldr + n, a.N - n, a.wide);
-    }
-};
-
-template <bool BF16, class Args>
-__device__ __forceinline__ void mx_finish(const Args& a, const MxAhead<Args>& in, int64_t m, int64_t n, f32x4 v) {
-    if (a.bias) v += in.b.get(a.bias_bf16, a.wide);
-    v = mx_activate<BF16>(v, a.act);
-    if (a.res) v += in.r.get(a.res_bf16, a.wide);
+// Row m, columns n .. n + 3: sums, bias and the residual loaded before.
+template <bool BF16, int ACT, bool WIDE, class Args>
+__device__ __forceinline__ void mx_finish(const Args& a, f32x4 v, f32x4 bias, const MxFour<WIDE>& res, int64_t m, int64_t n) {
+    v += bias;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = mx_act<BF16, ACT>(v[k]);
+    if (a.res) v += res.get(a.res_bf16);
     const int64_t at = m * a.ldy + n;
-    if (a.wide) {
+    if constexpr (WIDE) {
         if constexpr (BF16)
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
                 make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
@@ -209,59 +203,73 @@ struct MxSpot {
 // finds the lane whose experts hold the tile, and the lanes then take one of
 // those experts each.  Borders that do not ascend from 0 to M are cut to do
 // so, which keeps every access inside the buffers (the rows are then anyone's).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {   // inclusive sums over the lanes
+    auto add = [&](uint32_t moved) { v += moved; };
+    add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));   // row_shr:1, 2, 4, 8
+    add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+    add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+    add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+    add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast:15 to rows 1 and 3
+    add((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // row_bcast:31 to rows 2 and 3
+    return v;
+}
+
 template <int BM, int BN>
 __device__ __forceinline__ bool mx_spot(const MxGroupArgs& a, MxSpot& s) {
-    const int lane = threadIdx.x & 63, per = (a.E + 63) >> 6;
-    auto border = [&](int i) { return (int64_t)min(max((int64_t)a.offsets[i], (int64_t)0), a.M); };
-    auto rows = [&](int e, int64_t& lo) {
-        lo = border(e);
-        return max(border(e + 1), lo) - lo;
-    };
-    auto scan = [&](uint32_t v) {   // inclusive, over the wavefront
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t u = (uint32_t)__shfl_up((int)v, d);
-            if (lane >= d) v += u;
-        }
-        return v;
-    };
+    const int lane = threadIdx.x & 63, per = (a.E + 63) >> 6, M = (int)a.M;
     const uint32_t tiles_n = (uint32_t)((a.N + BN - 1) / BN);
+    // expert e's first row and rows, within [0, M]; none past the last expert
+    auto rows = [&](int e, int& lo) {
+        if (e >= a.E) return 0;
+        const int hi = min(max(a.offsets[e + 1], 0), M);
+        lo = min(max(a.offsets[e], 0), M);
+        return max(hi, lo) - lo;
+    };
+    auto lane_of = [](uint32_t v, int at) { return (uint32_t)__builtin_amdgcn_readlane((int)v, at); };
+    int lo = 0, n = 0;
     uint32_t mine = 0;
-    int64_t lo;
     for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e < a.E) mine += (uint32_t)((rows(e, lo) + BM - 1) / BM);
+        n = rows(lane * per + i, lo);
+        mine += (uint32_t)(n + BM - 1) / BM;
     }
-    uint32_t upto = scan(mine);
-    const uint32_t all = (uint32_t)__shfl((int)upto, 63);   // borders that ascend: at most gridDim.x / tiles_n
+    uint32_t upto = wave_scan(mine);
+    const uint32_t all = lane_of(upto, 63);   // borders that ascend: at most gridDim.x / tiles_n
     const uint32_t total = (uint32_t)min((uint64_t)all * tiles_n, (uint64_t)gridDim.x);
     if (blockIdx.x >= total) return false;
     // as in mx_tile: a contiguous run of the order per XCD
     const uint32_t q = total >> 3, rem = total & 7, x = blockIdx.x & 7;
     const uint32_t t = x * q + (x < rem ? x : rem) + (blockIdx.x >> 3), u = t / tiles_n;
     int at = __builtin_ctzll(__ballot(u < upto));   // the last lane's count is `all`, above u
-    uint32_t first = (uint32_t)__shfl((int)(upto - mine), at);
-    int e = at * per;
+    uint32_t first = lane_of(upto - mine, at);
+    s.e = at;
     if (per > 1) {
-        const uint32_t n = lane < per && e + lane < a.E ? (uint32_t)((rows(e + lane, lo) + BM - 1) / BM) : 0;
-        upto = scan(n);
+        const int base = at * per;
+        n = lane < per ? rows(base + lane, lo) : 0;
+        mine = (uint32_t)(n + BM - 1) / BM;
+        upto = wave_scan(mine);
         at = __builtin_ctzll(__ballot(u - first < upto));
-        e += at;
-        first += (uint32_t)__shfl((int)(upto - n), at);
+        first += lane_of(upto - mine, at);
+        s.e = base + at;
     }
-    e = __builtin_amdgcn_readfirstlane(e);
-    first = (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
-    const int64_t n_rows = rows(e, lo);
-    const uint32_t tiles_m = (uint32_t)((n_rows + BM - 1) / BM), local = t - first * tiles_n;
+    const int n_rows = (int)lane_of((uint32_t)n, at);
+    lo = (int)lane_of((uint32_t)lo, at);
+    const uint32_t tiles_m = (uint32_t)(n_rows + BM - 1) / BM, local = t - first * tiles_n;
     const uint32_t band = local / (4 * tiles_n), top = 4 * band;
     const uint32_t h = tiles_m - top < 4 ? tiles_m - top : 4, w = local - top * tiles_n;
-    s.e = e;
     s.tn = w / h;
     s.m0 = lo + (int64_t)(top + w % h) * BM;
     s.m1 = lo + n_rows;
     s.n0 = (int64_t)s.tn * BN;
     return true;
 }
+
+// The row of X that row p of Y takes, -1 for none.
+__device__ __forceinline__ bool mx_gathers(const MxGroupArgs& a) { return a.rows != nullptr; }
+__device__ __forceinline__ int mx_row(const MxGroupArgs& a, int64_t p, int64_t m1) {
+    const int i = p < m1 ? a.rows[p] : -1;
+    return (uint32_t)i < (uint32_t)a.x_rows ? i : -1;
+}
+
 template <int BM, int BN, class Args>
 __device__ __forceinline__ bool mx_spot(const Args& a, MxSpot& s) {
     uint32_t tm;
@@ -272,6 +280,8 @@ __device__ __forceinline__ bool mx_spot(const Args& a, MxSpot& s) {
     s.e = 0;
     return true;
 }
+__device__ __forceinline__ bool mx_gathers(const MxGemmArgs&) { return false; }
+__device__ __forceinline__ int mx_row(const MxGemmArgs&, int64_t, int64_t) { return -1; }
 
 // ------------------------------------------------------- few rows of X ----
 // 16 rows at most: streaming the weight once is the bound.  No LDS staging; a
@@ -342,15 +352,14 @@ __global__ void __launch_bounds__(1024) mx_gemm_skinny_kernel(Args a) {
 #pragma unroll
     for (int w = 1; w < NW; ++w) sum += red[w][i][j];
     if constexpr (kMxEpilogue<Args>) {
-        f32x4 v = {sum, 0.0f, 0.0f, 0.0f};
         auto as_f32 = [](const void* p, bool bf16, int64_t at) {
             return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[at] << 16)
                         : static_cast<const float*>(p)[at];
         };
-        if (a.bias) v[0] += as_f32(a.bias, a.bias_bf16, n0 + j);
-        v = mx_activate<BF16>(v, a.act);
-        if (a.res) v[0] += as_f32(a.res, a.res_bf16, i * a.ldr + n0 + j);
-        store_y<BF16>(a.y, i * a.ldy + n0 + j, v[0]);
+        if (a.bias) sum += as_f32(a.bias, a.bias_bf16, n0 + j);
+        mx_with_act(a.act, [&](auto Act) { sum = mx_act<BF16, decltype(Act)::value>(sum); });
+        if (a.res) sum += as_f32(a.res, a.res_bf16, i * a.ldr + n0 + j);
+        store_y<BF16>(a.y, i * a.ldy + n0 + j, sum);
     } else {
         store_y<BF16>(a.y, i * a.N + n0 + j, sum);
     }
@@ -398,6 +407,17 @@ struct Mover {
             off[q] = (uint32_t)r * (uint32_t)pitch + (uint32_t)piece * 16u;
         }
     }
+    // the same with row r of the tile being row at(r) of the `rows` at `base` (below 2^31 bytes in all), zeros for -1
+    template <class At>
+    __device__ __forceinline__ void gather(const void* base, int64_t rows, int64_t pitch, int w, At at) {
+        init(base, 0, rows, pitch, w);
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int r = (q * NW + w) * RPI + lane / SLOTS, i = at(r);
+            off[q] = i < 0 ? 0x80000000u : off[q] + (uint32_t)(i - r) * (uint32_t)pitch;
+        }
+    }
     // instructions [part Q / parts, (part + 1) Q / parts) of stage kt
     __device__ __forceinline__ void issue(char* lds, int kt, int part = 0, int parts = 1) {
 #pragma unroll
@@ -438,38 +458,66 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[TM][TN], const Mx
     }
 }
 
-// The same with an epilogue: a wavefront passes half a block (16 rows of 32
-// columns) at a time through its own part of LDS, so that a lane has four
-// neighbouring columns, and loads the next half's bias and residual before it
-// works on this one.
+// The same with an epilogue: a wavefront passes 32 rows of its blocks at a time
+// through its own part of LDS (`lds`, 128 TN * 32 bytes), so that a lane has four
+// neighbouring columns and a row of 64 is written in one piece.  The rows are
+// taken in a loop, U steps of it at a time with the next ones' residual on
+// its way.  Unrolled over the blocks, with a branch for the activation in each,
+// the code outgrew the instruction cache: 32768 x 4096 x 256 in 256x256 tiles
+// 250 us.
 template <int TM, int TN, bool BF16, class Args>
-__device__ __forceinline__ void finish_tile(const f32x16 (&acc)[TM][TN], const Args& a, char* lds, int wave, int64_t m0,
-                                            int64_t m1, int64_t n0, int64_t brow) {
-    const int lane = threadIdx.x & 63, half = lane >> 5, r = lane & 31;
-    float* red = reinterpret_cast<float*>(lds) + wave * (16 * 36);
-    MxAhead<Args> in[2][2];
-    auto ahead = [&](auto B) __attribute__((always_inline)) {
-        constexpr int b = decltype(B)::value / 2, h = decltype(B)::value % 2, i = b / TN, j = b % TN;
+__device__ __forceinline__ void finish_tile(const f32x16 (&acc)[TM][TN], const Args& a, float* lds, int64_t m0, int64_t m1,
+                                            int64_t n0, int64_t brow) {
+    constexpr int WN = 32 * TN, LPR = WN / 4, RPS = 64 / LPR, STEPS = 32 / RPS, U = 4;   // lanes a row, rows a step, steps
+    static_assert(STEPS % U == 0, "whole turns of the loop");
+    const int lane = threadIdx.x & 63, half = lane >> 5, r = lane & 31, row = lane / LPR, col = lane % LPR * 4;
+    const int64_t n = n0 + col;
+    auto rows = [&](int64_t first, auto Act, auto Wide) __attribute__((always_inline)) {
+        using Four = MxFour<decltype(Wide)::value>;
+        f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.bias) {
+            Four b;
+            b.load(a.bias, a.bias_bf16, brow + n, a.N - n);
+            bias = b.get(a.bias_bf16);
+        }
+        Four res[U], next[U];
+        auto ahead = [&](Four (&to)[U], int s) __attribute__((always_inline)) {
+            if (a.res) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int64_t m = m0 + i * 32 + h * 16 + q * 8 + (lane >> 3), n = n0 + j * 32 + (lane & 7) * 4;
-            if (m < m1 && n < a.N) in[h][q].load(a, brow, m, n);
+                for (int q = 0; q < U; ++q) {
+                    const int64_t m = first + (s + q) * RPS + row;
+                    if (m < m1) to[q].load(a.res, a.res_bf16, m * a.ldr + n, a.N - n);
+                }
+            }
+        };
+        ahead(res, 0);
+#pragma nounroll
+        for (int s = 0; s < STEPS && first + s * RPS < m1; s += U) {
+            if (s + U < STEPS) ahead(next, s + U);
+            f32x4 v[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) v[q] = *reinterpret_cast<const f32x4*>(lds + (row + (s + q) * RPS) * WN + col);
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const int64_t m = first + (s + q) * RPS + row;
+                if (m < m1) mx_finish<BF16, decltype(Act)::value>(a, v[q], bias, res[q], m, n);
+                res[q] = next[q];
+            }
         }
     };
-    ahead(std::integral_constant<int, 0>{});
-    gemm::static_for<2 * TM * TN>([&](auto B) {
-        constexpr int b = decltype(B)::value / 2, h = decltype(B)::value % 2, i = b / TN, j = b % TN;
-        if constexpr (decltype(B)::value + 1 < 2 * TM * TN) ahead(std::integral_constant<int, decltype(B)::value + 1>{});
-        asm volatile("" ::: "memory");   // a wavefront's LDS accesses run in order: the last half is read before this is written
+    gemm::static_for<TM>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        const int64_t first = m0 + i * 32;
+        if (first >= m1) return;
+        asm volatile("" ::: "memory");   // a wavefront's LDS accesses run in order: the last rows are read before these are written
 #pragma unroll
-        for (int e = 0; e < 8; ++e) red[(8 * (e >> 2) + 4 * half + (e & 3)) * 36 + r] = acc[i][j][8 * h + e];
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) lds[(8 * (e >> 2) + 4 * half + (e & 3)) * WN + j * 32 + r] = acc[i][j][e];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int64_t m = m0 + i * 32 + h * 16 + q * 8 + (lane >> 3), n = n0 + j * 32 + (lane & 7) * 4;
-            const f32x4 v = *reinterpret_cast<const f32x4*>(red + (q * 8 + (lane >> 3)) * 36 + (lane & 7) * 4);
-            if (m < m1 && n < a.N) mx_finish<BF16>(a, in[h][q], m, n, v);
-        }
+        if (n >= a.N) return;
+        if (a.wide) mx_with_act(a.act, [&](auto Act) { rows(first, Act, std::true_type{}); });
+        else mx_with_act(a.act, [&](auto Act) { rows(first, Act, std::false_type{}); });
     });
 }
 
@@ -481,7 +529,7 @@ __device__ __forceinline__ void finish_tile(const f32x16 (&acc)[TM][TN], const A
 // to start at a dword.  Row r's eight-byte piece p lies
 // at p ^ (r / 8 % 4), which spreads the 32 rows that a read takes over all
 // banks.
-template <int BM, int BN, int NW>
+template <int BM, int BN, int NW, bool GATHER = false>
 struct ScaleMover {
     // eight rows per instruction; with an uneven split some are moved twice, to the same place
     static constexpr int ROWS = BM + BN, QI = ROWS / 32, T = (QI + NW - 1) / NW;
@@ -489,6 +537,7 @@ struct ScaleMover {
     __amdgpu_buffer_rsrc_t rx, rw;
     uint32_t nb;
     int wave;
+    uint32_t from[GATHER ? 4 : 1][GATHER ? T : 1];   // where this lane's row of instruction t of a quarter starts
     __device__ __forceinline__ void init(const uint8_t* xs, int64_t xrows, const uint8_t* ws, int64_t wrows, int n, int w) {
         wave = w;
         nb = (uint32_t)n;
@@ -500,6 +549,23 @@ struct ScaleMover {
         rx = rsrc(xs, xrows);
         rw = rsrc(ws, wrows);
     }
+    // row r of X's tile is row at(r) of xs, zeros for -1
+    template <class At>
+    __device__ __forceinline__ void rows(At at) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const int row = (q * QI + (t * NW + wave) % QI) * 8;
+                if (row < BM) {
+                    const int i = at(row + lane / 8);
+                    from[q][t] = i < 0 ? 0x80000000u : (uint32_t)i * nb;
+                } else {
+                    from[q][t] = ((uint32_t)(row - BM) + lane / 8) * nb;
+                }
+            }
+    }
     // quarter q of group g
     __device__ __forceinline__ void issue(char* lds, int g, int q) {
         const uint32_t lane = threadIdx.x & 63;
@@ -508,8 +574,10 @@ struct ScaleMover {
         for (int t = 0; t < T; ++t) {
             const int i = q * QI + (t * NW + wave) % QI, row = i * 8;   // rows row .. row + 7, X's first
             const bool x = row < BM;
-            const uint32_t o = ((uint32_t)(x ? row : row - BM) + lane / 8) * nb + (uint32_t)g * 32u +
-                               ((((lane % 8) >> 1) ^ (uint32_t)(i & 3)) << 3) + (lane & 1) * 4;
+            uint32_t o;
+            if constexpr (GATHER) o = q == 0 ? from[0][t] : q == 1 ? from[1][t] : q == 2 ? from[2][t] : from[3][t];
+            else o = ((uint32_t)(x ? row : row - BM) + lane / 8) * nb;
+            o += (uint32_t)g * 32u + ((((lane % 8) >> 1) ^ (uint32_t)(i & 3)) << 3) + (lane & 1) * 4;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(x ? rx : rw, (lds_void*)(at + i * 256), 4, (int)o, 0, 0, 0);
         }
     }
@@ -528,20 +596,37 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(Args a)
     __shared__ __attribute__((aligned(1024))) char ssc[2 * (BM + BN) * 32];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / NWN, wn = wave % NWN, r = lane & 31, half = lane >> 5;
-    uint32_t tile_m, tile_n;
-    mx_tile((uint32_t)((a.M + BM - 1) / BM), (uint32_t)((a.N + BN - 1) / BN), tile_m, tile_n);
-    const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
+    MxSpot spot;
+    if (!mx_spot<BM, BN>(a, spot)) return;
+    const int64_t m0 = spot.m0, m1 = spot.m1, n0 = spot.n0;
     const int nb = (int)(a.K >> 5), nk = (nb + 7) >> 3;
+    const uint8_t *wp = a.wp, *wsc = a.ws;
+    if constexpr (kMxGrouped<Args>) {
+        wp += spot.e * a.N * (a.K >> 1);
+        wsc += spot.e * a.N * nb;
+    }
 
     Mover<BM, KS, NW> mx;
     Mover<BN, KS, NW> mw;
-    mx.init(a.xp, m0, a.M, a.K >> 1, wave);
-    mw.init(a.wp, n0, a.N, a.K >> 1, wave);
-    const uint8_t *xs = a.xs + m0 * nb, *ws = a.ws + n0 * nb;
+    [[maybe_unused]] auto x_row = [&](int row) __attribute__((always_inline)) { return mx_row(a, m0 + row, m1); };
+    if (!mx_gathers(a)) mx.init(a.xp, m0, m1, a.K >> 1, wave);
+    else if constexpr (kMxGrouped<Args>) mx.gather(a.xp, a.x_rows, a.K >> 1, wave, x_row);
+    mw.init(wp, n0, a.N, a.K >> 1, wave);
+    const uint8_t *xs = a.xs + m0 * nb, *ws = wsc + n0 * nb;
     const uint32_t sel = half ? 0x07050301u : 0x06040200u;
     uint64_t nx[TM], nw[TN];   // a stage's scale bytes
-    ScaleMover<BM, BN, NW> ms;
-    ms.init(xs, a.M - m0, ws, a.N - n0, nb, wave);
+    ScaleMover<BM, BN, NW, kMxGrouped<Args>> ms;
+    if constexpr (kMxGrouped<Args>) {
+        if (a.rows) {
+            ms.init(a.xs, a.x_rows, ws, a.N - n0, nb, wave);
+            ms.rows(x_row);
+        } else {
+            ms.init(xs, m1 - m0, ws, a.N - n0, nb, wave);
+            ms.rows([](int row) { return row; });
+        }
+    } else {
+        ms.init(xs, m1 - m0, ws, a.N - n0, nb, wave);
+    }
     auto load_scales = [&](int kt) __attribute__((always_inline)) {
         const char* g = ssc + ((kt >> 2) & 1) * (BM + BN) * 32 + r * 32 + (((kt & 3) ^ ((r >> 3) & 3)) << 3);
 #pragma unroll
@@ -636,8 +721,11 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(Args a)
 
     if constexpr (kMxEpilogue<Args>) {
         lds_barrier();   // every wavefront is done with the stages
-        static_assert(sizeof(sw0) >= NW * 16 * 36 * 4, "half a block of every wavefront");
-        finish_tile<TM, TN, BF16>(acc, a, sw0, wave, m0 + wm * WM, a.M, n0 + wn * WN, 0);
+        constexpr int PER = sizeof(sw0) / (32 * WN * 4);   // wavefronts in one of the buffers of W
+        static_assert(2 * PER >= NW, "32 rows of every wavefront");
+        char* at = (wave < PER ? sw0 : sw1) + wave % PER * (32 * WN * 4);
+        finish_tile<TM, TN, BF16>(acc, a, reinterpret_cast<float*>(at), m0 + wm * WM, m1, n0 + wn * WN,
+                                  (int64_t)spot.e * a.N);
     } else {
         store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
     }
@@ -781,17 +869,8 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
         wp += spot.e * a.N * (a.K >> 1);
         ws += spot.e * a.N * nb;
     }
-    // this tile's row r of X, -1 for none (grouped products that gather)
-    const bool gather = [&] { if constexpr (kMxGrouped<Args>) return a.rows != nullptr; else return false; }();
-    auto x_row = [&](int r) __attribute__((always_inline)) {
-        int i = -1;
-        if constexpr (kMxGrouped<Args>)
-            if (m0 + r < m1) {
-                i = a.rows[m0 + r];
-                if ((uint32_t)i >= (uint32_t)a.x_rows) i = -1;
-            }
-        return i;
-    };
+    const bool gather = mx_gathers(a);
+    auto x_row = [&](int row) __attribute__((always_inline)) { return mx_row(a, m0 + row, m1); };
 
     RingMover<BM, XR, XSUB, NW> mx;
     RingMover<BN, WB, 1, NW> mw;
@@ -877,7 +956,8 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
 #pragma unroll
         for (int i = 0; i < TM; ++i) xf[u & 1][i] = *reinterpret_cast<const u32x4*>(st + at + i * 32 * XR);
     };
-    auto compute = [&](int kt, const char* st, auto Slot) __attribute__((always_inline)) {
+    // Of the wavefront's blocks of 32 rows the first `live` are multiplied.
+    auto compute = [&](int kt, const char* st, auto Slot, auto live) __attribute__((always_inline)) {
         constexpr int p = decltype(Slot)::value;
         gemm::static_for<UNITS>([&](auto U) {
             constexpr int u = decltype(U)::value, t = A4 ? u : u / 4, q = u % 4;
@@ -898,7 +978,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
                     const bf16x8 w = unpack8(wf[t & 1][j][q], scale_f32(in ? cw[p][t][j] : 0u));
 #pragma unroll
                     for (int i = 0; i < TM; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, xf[u & 1][i]), w,
+                        if (i < live) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, xf[u & 1][i]), w,
                                                                             acc[i][j], 0, 0, 0);
                 }
             }
@@ -920,39 +1000,55 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
         wait_vmcnt<decltype(Allowed)::value>();
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // stage landed; the previous one is read
     };
-    int kt = 0;
-    for (; kt + NST <= nk; kt += NST)
-        gemm::static_for<NST>([&](auto S) {
+    auto stages = [&](auto live) __attribute__((always_inline)) {
+        int kt = 0;
+        for (; kt + NST <= nk; kt += NST)
+            gemm::static_for<NST>([&](auto S) {
+                constexpr int p = decltype(S)::value;
+                using Prev = std::integral_constant<int, (p + NST - 1) % NST>;
+                arrive(std::integral_constant<int, (NST - 2) * LPW + (p >= 1 && p <= NST - 2 ? SPG : 0)>{});
+                if constexpr (p == 0) {
+                    read_scales(kt / NST);
+                    read_unit(buf(S), U0{});
+                    __builtin_amdgcn_sched_barrier(0);
+                    issue_scales((kt / NST) + 1);
+                } else {
+                    read_unit(buf(S), U0{});
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                issue(kt + p + NST - 1, buf(Prev{}));
+                compute(kt + p, buf(S), S, live);
+            });
+        gemm::static_for<NST - 1>([&](auto S) {   // the stages left, all loaded already
             constexpr int p = decltype(S)::value;
-            using Prev = std::integral_constant<int, (p + NST - 1) % NST>;
-            arrive(std::integral_constant<int, (NST - 2) * LPW + (p >= 1 && p <= NST - 2 ? SPG : 0)>{});
-            if constexpr (p == 0) {
-                read_scales(kt / NST);
+            if (kt + p < nk) {
+                arrive(std::integral_constant<int, (NST - 2 - p) * LPW>{});
+                if constexpr (p == 0) read_scales(kt / NST);
                 read_unit(buf(S), U0{});
-                __builtin_amdgcn_sched_barrier(0);
-                issue_scales((kt / NST) + 1);
-            } else {
-                read_unit(buf(S), U0{});
-                __builtin_amdgcn_sched_barrier(0);
+                compute(kt + p, buf(S), S, live);
             }
-            issue(kt + p + NST - 1, buf(Prev{}));
-            compute(kt + p, buf(S), S);
         });
-    gemm::static_for<NST - 1>([&](auto S) {   // the stages left, all loaded already
-        constexpr int p = decltype(S)::value;
-        if (kt + p < nk) {
-            arrive(std::integral_constant<int, (NST - 2 - p) * LPW>{});
-            if constexpr (p == 0) read_scales(kt / NST);
-            read_unit(buf(S), U0{});
-            compute(kt + p, buf(S), S);
-        }
-    });
+    };
+    using All = std::integral_constant<int, TM>;
+    // Blocks past the tile's last row (an expert's last tile is part-filled; with 256 skewed rows an expert a third of
+    // all blocks) are skipped in a loop of its own: 32768 x 4096 x 2048 over 128 experts 650 -> 591 us in the bf16
+    // form's tallest tile.  A branch in the one loop costs full tiles 10%.
+    if constexpr (kMxEpilogue<Args> && !A4 && TM >= 4) {
+        const int64_t rows = m1 - m0 - wm * WM;
+        if (rows <= WM - 32) stages(rows <= 0 ? 0 : ((int)rows + 31) >> 5);
+        else stages(All{});
+    } else {
+        stages(All{});
+    }
     wait_vmcnt<0>();
 
     if constexpr (kMxEpilogue<Args> && NWK == 1) {
         lds_barrier();   // every wavefront is done with the stages
-        const int64_t brow = (int64_t)spot.e * a.N;
-        finish_tile<TM, TN, BF16>(acc, a, st0, wave, m0 + wm * WM, m1, n0 + wn * WN, brow);
+        constexpr int PER = STAGE / (32 * WN * 4);   // wavefronts in a stage
+        static_assert(3 * PER >= NW, "32 rows of every wavefront");
+        char* at = (wave < PER ? st0 : wave < 2 * PER ? st1 : st2) + wave % PER * (32 * WN * 4);
+        finish_tile<TM, TN, BF16>(acc, a, reinterpret_cast<float*>(at), m0 + wm * WM, m1, n0 + wn * WN,
+                                  (int64_t)spot.e * a.N);
         return;
     }
     // Half a block at a time through LDS: every set's sums, then all threads add
@@ -962,8 +1058,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (BF16 ? 7 : 15)) == 0;
     const int set = wm * NWN + wn;
     [[maybe_unused]] const int64_t brow = (int64_t)spot.e * a.N;
-    using In = std::conditional_t<kMxEpilogue<Args>, MxAhead<Args>, int>;
-    [[maybe_unused]] In in[PER];
+    [[maybe_unused]] MxFour<true> bin[PER], rin[PER];
     gemm::static_for<2 * TM * TN>([&](auto B) {
         constexpr int b = decltype(B)::value / 2, h = decltype(B)::value % 2, i = b / TN, j = b % TN;
         if constexpr (kMxEpilogue<Args>) {   // bias and residual, on their way during the barriers
@@ -971,7 +1066,10 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
             for (int q = 0; q < PER; ++q) {
                 const int t = (q * NWK + wk) * 64 + lane, row = t >> 3;
                 const int64_t m = m0 + wm * WM + i * 32 + h * 16 + row, n = n0 + wn * WN + j * 32 + (t & 7) * 4;
-                if (row < 16 && m < m1 && n < a.N) in[q].load(a, brow, m, n);
+                if (a.wide && row < 16 && m < m1 && n < a.N) {
+                    if (a.bias) bin[q].load(a.bias, a.bias_bf16, brow + n, 4);
+                    if (a.res) rin[q].load(a.res, a.res_bf16, m * a.ldr + n, 4);
+                }
             }
         }
         __syncthreads();
@@ -988,7 +1086,19 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
 #pragma unroll
             for (int w = 1; w < NWK; ++w) v += *reinterpret_cast<const f32x4*>(red + ((set * NWK + w) * 16 + row) * 36 + c);
             if constexpr (kMxEpilogue<Args>) {
-                mx_finish<BF16>(a, in[q], m, n, v);
+                f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (a.wide) {
+                    if (a.bias) bias = bin[q].get(a.bias_bf16);
+                    mx_with_act(a.act, [&](auto Act) { mx_finish<BF16, decltype(Act)::value>(a, v, bias, rin[q], m, n); });
+                } else {
+                    MxFour<false> b, res;
+                    if (a.bias) {
+                        b.load(a.bias, a.bias_bf16, brow + n, a.N - n);
+                        bias = b.get(a.bias_bf16);
+                    }
+                    if (a.res) res.load(a.res, a.res_bf16, m * a.ldr + n, a.N - n);
+                    mx_with_act(a.act, [&](auto Act) { mx_finish<BF16, decltype(Act)::value>(a, v, bias, res, m, n); });
+                }
                 continue;
             } else if (wide) {
                 if constexpr (BF16)
