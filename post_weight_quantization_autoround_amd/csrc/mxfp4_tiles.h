@@ -20,6 +20,7 @@ using gemm::gbl_void;
 using gemm::lds_barrier;
 using gemm::lds_void;
 using gemm::wait_vmcnt;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -117,59 +118,56 @@ __device__ __forceinline__ void mx_with_act(int act, F f) {
     else f(std::integral_constant<int, kMxGeluTanh>{});
 }
 
-// Four neighbouring columns of a row: WIDE (N and the row strides multiples of
-// four, addresses aligned to four elements) in one access, else one by one up
-// to column N.
-template <bool WIDE>
+// Four neighbouring columns of a row, `left` >= 1 of them before column N: in
+// one access where a.wide tells that it is aligned and N a multiple of four,
+// else one by one (past N the last one again, which no one uses).
 struct MxFour {
     u32x4 raw;
-    __device__ __forceinline__ void load(const void* p, bool bf16, int64_t at, int64_t left) {
-        if constexpr (WIDE) {
+    __device__ __forceinline__ void load(const void* p, bool bf16, bool wide, int64_t left) {
+        if (wide) {
             if (bf16) {
-                const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
-                raw[0] = v.x;
-                raw[1] = v.y;
+                const u32x2 v = *static_cast<const u32x2*>(p);
+                raw[0] = v[0];
+                raw[1] = v[1];
             } else {
-                raw = *reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + at);
+                raw = *static_cast<const u32x4*>(p);
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < left)
-                    raw[k] = bf16 ? (uint32_t)static_cast<const uint16_t*>(p)[at + k]
-                                  : static_cast<const uint32_t*>(p)[at + k];
+            for (int k = 0; k < 4; ++k) {
+                const int64_t at = k < left ? k : left - 1;
+                raw[k] = bf16 ? (uint32_t)static_cast<const uint16_t*>(p)[at] << 16 : static_cast<const uint32_t*>(p)[at];
+            }
         }
     }
-    __device__ __forceinline__ f32x4 get(bool bf16) const {
+    __device__ __forceinline__ f32x4 get(bool bf16, bool wide) const {
+        const bool pairs = bf16 && wide;
         f32x4 v;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t both = raw[k >> 1];   // of the packed form
-            const uint32_t bits = !bf16 ? raw[k] : !WIDE ? raw[k] << 16 : k & 1 ? both & 0xFFFF0000u : both << 16;
-            v[k] = __uint_as_float(bits);
-        }
+        v[0] = __uint_as_float(pairs ? raw[0] << 16 : raw[0]);
+        v[1] = __uint_as_float(pairs ? raw[0] & 0xFFFF0000u : raw[1]);
+        v[2] = __uint_as_float(pairs ? raw[1] << 16 : raw[2]);
+        v[3] = __uint_as_float(pairs ? raw[1] & 0xFFFF0000u : raw[3]);
         return v;
     }
 };
 
-// Row m, columns n .. n + 3: sums, bias and the residual loaded before.
-template <bool BF16, int ACT, bool WIDE, class Args>
-__device__ __forceinline__ void mx_finish(const Args& a, f32x4 v, f32x4 bias, const MxFour<WIDE>& res, int64_t m, int64_t n) {
-    v += bias;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = mx_act<BF16, ACT>(v[k]);
-    if (a.res) v += res.get(a.res_bf16);
-    const int64_t at = m * a.ldy + n;
-    if constexpr (WIDE) {
-        if constexpr (BF16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        else
-            *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
+// STREAM: past the L2, whose lines the large tiles' operands need (32768 x 4096
+// x 2048 over 128 experts 4 to 8% shorter).
+template <bool BF16, bool STREAM>
+__device__ __forceinline__ void mx_store_four(void* y, f32x4 v, bool wide, int64_t left) {
+    if (wide) {
+        if constexpr (BF16) {
+            const u32x2 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            if constexpr (STREAM) __builtin_nontemporal_store(o, static_cast<u32x2*>(y));
+            else *static_cast<u32x2*>(y) = o;
+        } else {
+            if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<f32x4*>(y));
+            else *static_cast<f32x4*>(y) = v;
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (n + k < a.N) store_y<BF16>(a.y, at + k, v[k]);
+            if (k < left) store_y<BF16>(y, k, v[k]);
     }
 }
 
@@ -226,11 +224,16 @@ __device__ __forceinline__ bool mx_spot(const MxGroupArgs& a, MxSpot& s) {
         return max(hi, lo) - lo;
     };
     auto lane_of = [](uint32_t v, int at) { return (uint32_t)__builtin_amdgcn_readlane((int)v, at); };
-    int lo = 0, n = 0;
+    constexpr int HELD = 4;   // experts a lane keeps in registers
+    int lo[HELD], n[HELD];
     uint32_t mine = 0;
-    for (int i = 0; i < per; ++i) {
-        n = rows(lane * per + i, lo);
-        mine += (uint32_t)(n + BM - 1) / BM;
+    if (per <= HELD) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) n[i] = i < per ? rows(lane * per + i, lo[i]) : 0;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) mine += (uint32_t)(n[i] + BM - 1) / BM;
+    } else {
+        for (int i = 0; i < per; ++i) mine += (uint32_t)(rows(lane * per + i, lo[0]) + BM - 1) / BM;
     }
     uint32_t upto = wave_scan(mine);
     const uint32_t all = lane_of(upto, 63);   // borders that ascend: at most gridDim.x / tiles_n
@@ -241,24 +244,38 @@ __device__ __forceinline__ bool mx_spot(const MxGroupArgs& a, MxSpot& s) {
     const uint32_t t = x * q + (x < rem ? x : rem) + (blockIdx.x >> 3), u = t / tiles_n;
     int at = __builtin_ctzll(__ballot(u < upto));   // the last lane's count is `all`, above u
     uint32_t first = lane_of(upto - mine, at);
-    s.e = at;
-    if (per > 1) {
-        const int base = at * per;
-        n = lane < per ? rows(base + lane, lo) : 0;
-        mine = (uint32_t)(n + BM - 1) / BM;
+    int n_rows = 0, row0 = 0;
+    s.e = at * per;
+    if (per <= HELD) {
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int rows_i = (int)lane_of((uint32_t)n[i], at), row_i = (int)lane_of((uint32_t)lo[i], at);
+            const uint32_t tiles_i = (uint32_t)(rows_i + BM - 1) / BM;
+            if (!found && u - first < tiles_i) {
+                found = true;
+                n_rows = rows_i;
+                row0 = row_i;
+                s.e += i;
+            }
+            if (!found) first += tiles_i;
+        }
+    } else {
+        n[0] = lane < per ? rows(s.e + lane, lo[0]) : 0;
+        mine = (uint32_t)(n[0] + BM - 1) / BM;
         upto = wave_scan(mine);
         at = __builtin_ctzll(__ballot(u - first < upto));
         first += lane_of(upto - mine, at);
-        s.e = base + at;
+        n_rows = (int)lane_of((uint32_t)n[0], at);
+        row0 = (int)lane_of((uint32_t)lo[0], at);
+        s.e += at;
     }
-    const int n_rows = (int)lane_of((uint32_t)n, at);
-    lo = (int)lane_of((uint32_t)lo, at);
     const uint32_t tiles_m = (uint32_t)(n_rows + BM - 1) / BM, local = t - first * tiles_n;
     const uint32_t band = local / (4 * tiles_n), top = 4 * band;
     const uint32_t h = tiles_m - top < 4 ? tiles_m - top : 4, w = local - top * tiles_n;
     s.tn = w / h;
-    s.m0 = lo + (int64_t)(top + w % h) * BM;
-    s.m1 = lo + n_rows;
+    s.m0 = row0 + (int64_t)(top + w % h) * BM;
+    s.m1 = row0 + n_rows;
     s.n0 = (int64_t)s.tn * BN;
     return true;
 }
@@ -458,66 +475,95 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[TM][TN], const Mx
     }
 }
 
+// Block I of a wavefront's, read in a branch of its own: the compiler would
+// merge the branches over the blocks into one that indexes them, through memory.
+// (The nops cover the last product's write-back, which the compiler cannot see
+// through the assembly.)
+template <int I>
+__device__ __forceinline__ f32x16 mx_apart(f32x16 block) {
+    asm volatile("s_nop 15\n\ts_nop 7 ; block %1" : "+v"(block) : "n"(I));
+    return block;
+}
+
 // The same with an epilogue: a wavefront passes 32 rows of its blocks at a time
 // through its own part of LDS (`lds`, 128 TN * 32 bytes), so that a lane has four
-// neighbouring columns and a row of 64 is written in one piece.  The rows are
-// taken in a loop, U steps of it at a time with the next ones' residual on
-// its way.  Unrolled over the blocks, with a branch for the activation in each,
-// the code outgrew the instruction cache: 32768 x 4096 x 256 in 256x256 tiles
-// 250 us.
+// neighbouring columns and a row of 64 is written in one piece, U steps of rows
+// at a time with the next ones' residual on their way.  One branch for the
+// activation ahead of all, then loops whose code is there once: unrolled over
+// the blocks the code outgrows the instruction cache, and a 256x256 tile spent
+// 8 to 17 us here.
 template <int TM, int TN, bool BF16, class Args>
 __device__ __forceinline__ void finish_tile(const f32x16 (&acc)[TM][TN], const Args& a, float* lds, int64_t m0, int64_t m1,
                                             int64_t n0, int64_t brow) {
     constexpr int WN = 32 * TN, LPR = WN / 4, RPS = 64 / LPR, STEPS = 32 / RPS, U = 4;   // lanes a row, rows a step, steps
+    constexpr int64_t ES = BF16 ? 2 : 4;
     static_assert(STEPS % U == 0, "whole turns of the loop");
     const int lane = threadIdx.x & 63, half = lane >> 5, r = lane & 31, row = lane / LPR, col = lane % LPR * 4;
-    const int64_t n = n0 + col;
-    auto rows = [&](int64_t first, auto Act, auto Wide) __attribute__((always_inline)) {
-        using Four = MxFour<decltype(Wide)::value>;
-        f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (a.bias) {
-            Four b;
-            b.load(a.bias, a.bias_bf16, brow + n, a.N - n);
-            bias = b.get(a.bias_bf16);
-        }
-        Four res[U], next[U];
-        auto ahead = [&](Four (&to)[U], int s) __attribute__((always_inline)) {
+    const int64_t n = n0 + col, left = a.N - n;
+    const int tile_rows = (int)max(min(m1 - m0, (int64_t)TM * 32), (int64_t)0);   // the wavefront's
+    const int rows = left > 0 ? tile_rows - row : 0;                              // from this lane's first on
+    const int64_t r_size = a.res_bf16 ? 2 : 4, y_step = RPS * a.ldy * ES, r_step = RPS * a.ldr * r_size;
+    f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.bias && left > 0) {
+        MxFour b;
+        b.load(static_cast<const char*>(a.bias) + (brow + n) * (a.bias_bf16 ? 2 : 4), a.bias_bf16, a.wide, left);
+        bias = b.get(a.bias_bf16, a.wide);
+    }
+    // The halves of a wavefront write rows four apart, which meet in the same banks of LDS: a row whose number has bit 2
+    // set holds its columns 32 places on (64 columns), so that they do not.  Step s reads rows RPS s + row.
+    constexpr int TURN = TN == 2 ? 32 : 0;
+    static_assert(TN != 2 || (RPS == 4 && U % 2 == 0), "bit 2 of a step's rows is the step's parity");
+    const float *from = lds + row * WN + col, *from_odd = lds + row * WN + (col ^ TURN);
+    mx_with_act(a.act, [&](auto Act) {
+        char* y = static_cast<char*>(a.y) + ((m0 + row) * a.ldy + n) * ES;
+        const char* res = static_cast<const char*>(a.res) + ((m0 + row) * a.ldr + n) * r_size;
+        MxFour now[U], next[U];
+        auto ahead = [&](int done) __attribute__((always_inline)) {   // rows done + RPS q
             if (a.res) {
 #pragma unroll
                 for (int q = 0; q < U; ++q) {
-                    const int64_t m = first + (s + q) * RPS + row;
-                    if (m < m1) to[q].load(a.res, a.res_bf16, m * a.ldr + n, a.N - n);
+                    if (done + q * RPS < rows) next[q].load(res, a.res_bf16, a.wide, left);
+                    res += r_step;
                 }
             }
         };
-        ahead(res, 0);
+        ahead(0);
 #pragma nounroll
-        for (int s = 0; s < STEPS && first + s * RPS < m1; s += U) {
-            if (s + U < STEPS) ahead(next, s + U);
-            f32x4 v[U];
+        for (int i = 0; i < TM; ++i) {
+            if (i * 32 >= tile_rows) break;
+            asm volatile("" ::: "memory");   // a wavefront's LDS accesses run in order: the last rows are read before these are written
+            gemm::static_for<TM>([&](auto I) {
+                if (i == decltype(I)::value) {
 #pragma unroll
-            for (int q = 0; q < U; ++q) v[q] = *reinterpret_cast<const f32x4*>(lds + (row + (s + q) * RPS) * WN + col);
+                    for (int j = 0; j < TN; ++j) {
+                        const f32x16 block = mx_apart<decltype(I)::value * TN>(acc[decltype(I)::value][j]);
+                        float* to = lds + 4 * half * WN + ((j * 32 + r) ^ (half ? TURN : 0));
 #pragma unroll
-            for (int q = 0; q < U; ++q) {
-                const int64_t m = first + (s + q) * RPS + row;
-                if (m < m1) mx_finish<BF16, decltype(Act)::value>(a, v[q], bias, res[q], m, n);
-                res[q] = next[q];
+                        for (int e = 0; e < 16; ++e) to[(8 * (e >> 2) + (e & 3)) * WN] = block[e];
+                    }
+                }
+            });
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma nounroll
+            for (int s = 0; s < STEPS; s += U) {
+                const int done = i * 32 + s * RPS;
+#pragma unroll
+                for (int q = 0; q < U; ++q) now[q] = next[q];
+                ahead(done + U * RPS);
+                f32x4 v[U];
+#pragma unroll
+                for (int q = 0; q < U; ++q) v[q] = *reinterpret_cast<const f32x4*>((q & 1 ? from_odd : from) + (s + q) * RPS * WN);
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    v[q] += bias;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[q][k] = mx_act<BF16, decltype(Act)::value>(v[q][k]);
+                    if (a.res) v[q] += now[q].get(a.res_bf16, a.wide);
+                    if (done + q * RPS < rows) mx_store_four<BF16, true>(y, v[q], a.wide, left);
+                    y += y_step;
+                }
             }
         }
-    };
-    gemm::static_for<TM>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        const int64_t first = m0 + i * 32;
-        if (first >= m1) return;
-        asm volatile("" ::: "memory");   // a wavefront's LDS accesses run in order: the last rows are read before these are written
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) lds[(8 * (e >> 2) + 4 * half + (e & 3)) * WN + j * 32 + r] = acc[i][j][e];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (n >= a.N) return;
-        if (a.wide) mx_with_act(a.act, [&](auto Act) { rows(first, Act, std::true_type{}); });
-        else mx_with_act(a.act, [&](auto Act) { rows(first, Act, std::false_type{}); });
     });
 }
 
@@ -1057,50 +1103,75 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     float* red = reinterpret_cast<float*>(st0);
     const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (BF16 ? 7 : 15)) == 0;
     const int set = wm * NWN + wn;
-    [[maybe_unused]] const int64_t brow = (int64_t)spot.e * a.N;
-    [[maybe_unused]] MxFour<true> bin[PER], rin[PER];
-    gemm::static_for<2 * TM * TN>([&](auto B) {
-        constexpr int b = decltype(B)::value / 2, h = decltype(B)::value % 2, i = b / TN, j = b % TN;
-        if constexpr (kMxEpilogue<Args>) {   // bias and residual, on their way during the barriers
-#pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                const int t = (q * NWK + wk) * 64 + lane, row = t >> 3;
-                const int64_t m = m0 + wm * WM + i * 32 + h * 16 + row, n = n0 + wn * WN + j * 32 + (t & 7) * 4;
-                if (a.wide && row < 16 && m < m1 && n < a.N) {
-                    if (a.bias) bin[q].load(a.bias, a.bias_bf16, brow + n, 4);
-                    if (a.res) rin[q].load(a.res, a.res_bf16, m * a.ldr + n, 4);
-                }
-            }
-        }
-        __syncthreads();
+    auto put = [&](const f32x16& block, int h0) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            red[((set * NWK + wk) * 16 + 8 * (e >> 2) + 4 * half + (e & 3)) * 36 + r] = acc[i][j][8 * h + e];
+            red[((set * NWK + wk) * 16 + 8 * (e >> 2) + 4 * half + (e & 3)) * 36 + r] = block[h0 + e];
+    };
+    auto sums = [&](int row, int c) __attribute__((always_inline)) {
+        f32x4 v = *reinterpret_cast<const f32x4*>(red + (set * NWK * 16 + row) * 36 + c);
+#pragma unroll
+        for (int w = 1; w < NWK; ++w) v += *reinterpret_cast<const f32x4*>(red + ((set * NWK + w) * 16 + row) * 36 + c);
+        return v;
+    };
+    if constexpr (kMxEpilogue<Args>) {   // one branch for the activation, then code that is there once, as in finish_tile
+        const int64_t brow = (int64_t)spot.e * a.N;
+        mx_with_act(a.act, [&](auto Act) {
+            constexpr int UNROLL = 2 * TM * TN <= 4 ? 4 : 1;
+#pragma unroll UNROLL
+            for (int b = 0; b < 2 * TM * TN; ++b) {
+                const int h = b & 1, i = (b >> 1) / TN, j = (b >> 1) % TN;
+                MxFour bias[PER], res[PER];   // on their way during the barriers
+                int64_t m[PER], n[PER];
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    const int t = (q * NWK + wk) * 64 + lane;
+                    m[q] = m0 + wm * WM + i * 32 + h * 16 + (t >> 3);
+                    n[q] = n0 + wn * WN + j * 32 + (t & 7) * 4;
+                    if (t >> 3 >= 16 || n[q] >= a.N) m[q] = m1;   // nothing of this lane's
+                    if (m[q] < m1) {
+                        if (a.bias)
+                            bias[q].load(static_cast<const char*>(a.bias) + (brow + n[q]) * (a.bias_bf16 ? 2 : 4), a.bias_bf16,
+                                         a.wide, a.N - n[q]);
+                        if (a.res)
+                            res[q].load(static_cast<const char*>(a.res) + (m[q] * a.ldr + n[q]) * (a.res_bf16 ? 2 : 4),
+                                        a.res_bf16, a.wide, a.N - n[q]);
+                    }
+                }
+                __syncthreads();
+                gemm::static_for<2 * TM * TN>([&](auto B) {
+                    constexpr int p = decltype(B)::value;
+                    if (b == p) put(mx_apart<p>(acc[p / 2 / TN][p / 2 % TN]), 8 * (p % 2));
+                });
+                __syncthreads();
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    const int t = (q * NWK + wk) * 64 + lane;
+                    if (m[q] >= m1) continue;
+                    f32x4 v = sums(t >> 3, (t & 7) * 4);
+                    if (a.bias) v += bias[q].get(a.bias_bf16, a.wide);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = mx_act<BF16, decltype(Act)::value>(v[k]);
+                    if (a.res) v += res[q].get(a.res_bf16, a.wide);
+                    mx_store_four<BF16, false>(static_cast<char*>(a.y) + (m[q] * a.ldy + n[q]) * (BF16 ? 2 : 4), v, a.wide,
+                                               a.N - n[q]);
+                }
+            }
+        });
+        return;
+    }
+    gemm::static_for<2 * TM * TN>([&](auto B) {
+        constexpr int b = decltype(B)::value / 2, h = decltype(B)::value % 2, i = b / TN, j = b % TN;
+        __syncthreads();
+        put(acc[i][j], 8 * h);
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
             const int t = (q * NWK + wk) * 64 + lane, row = t >> 3, c = (t & 7) * 4;
             const int64_t m = m0 + wm * WM + i * 32 + h * 16 + row, n = n0 + wn * WN + j * 32 + c;
-            if (row >= 16 || m >= m1 || n >= a.N) continue;
-            f32x4 v = *reinterpret_cast<const f32x4*>(red + (set * NWK * 16 + row) * 36 + c);
-#pragma unroll
-            for (int w = 1; w < NWK; ++w) v += *reinterpret_cast<const f32x4*>(red + ((set * NWK + w) * 16 + row) * 36 + c);
-            if constexpr (kMxEpilogue<Args>) {
-                f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (a.wide) {
-                    if (a.bias) bias = bin[q].get(a.bias_bf16);
-                    mx_with_act(a.act, [&](auto Act) { mx_finish<BF16, decltype(Act)::value>(a, v, bias, rin[q], m, n); });
-                } else {
-                    MxFour<false> b, res;
-                    if (a.bias) {
-                        b.load(a.bias, a.bias_bf16, brow + n, a.N - n);
-                        bias = b.get(a.bias_bf16);
-                    }
-                    if (a.res) res.load(a.res, a.res_bf16, m * a.ldr + n, a.N - n);
-                    mx_with_act(a.act, [&](auto Act) { mx_finish<BF16, decltype(Act)::value>(a, v, bias, res, m, n); });
-                }
-                continue;
-            } else if (wide) {
+            if (row >= 16 || m >= a.M || n >= a.N) continue;
+            const f32x4 v = sums(row, c);
+            if (wide) {
                 if constexpr (BF16)
                     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + m * a.N + n) =
                         make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
