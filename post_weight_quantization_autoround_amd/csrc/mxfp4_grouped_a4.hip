@@ -7,13 +7,13 @@ namespace ar {
 // quarter of the time, so larger tiles pay earlier.  The tile kernels take K in
 // multiples of 128 and scales at dword addresses; the ring takes the rest.
 // Measured (us, rows x experts x N x K with skewed groups, the choice first):
-//   512 x 128 x 2048 x 4096 (4 rows an expert): 64x128 101, 32x64 102, 128x128 106 (the weight streams in 101)
-//   256 x 64 x 2048 x 2048 (4): 64x128 26, 128x128 27, 32x64 34
-//   128 x 8 x 4096 x 4096 (16): 32x64 14.8, 64x128 16.0, 128x128 17.4
-//   1024 x 32 x 4096 x 4096 (32): 128x128 60-66, 64x128 68, 32x64 76
-//   8192 x 64 x 4096 x 2048 (128): 128x128 124, 256x256 125, 64x128 138
-//   32768 x 128 x 4096 x 2048 (256): 256x256 330, 128x128 388, 64x128 525
-//   32768 x 32 x 4096 x 4096 (1024): 256x256 400, 128x128 458
+//   512 x 128 x 2048 x 4096 (4 rows an expert): 64x128 104, 128x128 107, 32x64 113 (the weight streams in 101)
+//   256 x 64 x 2048 x 2048 (4): 64x128 27, 128x128 29, 32x64 37
+//   128 x 8 x 4096 x 4096 (16): 32x64 15.2, 64x128 16.5, 128x128 17.7
+//   1024 x 32 x 4096 x 4096 (32): 128x128 58, 64x128 68, 256x256 68
+//   8192 x 64 x 4096 x 2048 (128): 128x128 112, 256x256 113, 64x128 134
+//   32768 x 128 x 4096 x 2048 (256): 256x256 303, 128x128 361, 64x128 490
+//   32768 x 32 x 4096 x 4096 (1024): 256x256 372, 128x128 447
 //   K 2080: 3000 x 16 x 4096 (188): 128x128 67, 64x64 77, 32x64 96; 700 x 5 x 1000 (140): 32x64 10, 64x64 11
 hipError_t launch_mx_grouped_a4(const MxGroupArgs& a, hipStream_t stream) {
     const bool aligned = a.K % 128 == 0 && a.K >= 256 &&

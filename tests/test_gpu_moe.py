@@ -269,7 +269,9 @@ def test_grouped_exact(ar, sizes, lead, trail, n, k, gather):
 # mean rows an expert and widths that lead to each of the tiles, with skewed groups
 TILED = [(5, 8, 4100, 512), (40, 8, 9000, 288), (70, 16, 4200, 1504), (130, 8, 9000, 288), (300, 8, 4200, 2016),
          (300, 6, 9000, 416), (600, 5, 4200, 1184), (1100, 4, 4200, 2304), (1100, 4, 9000, 288), (200, 64, 520, 640),
-         (24, 128, 520, 2400), (2, 200, 520, 1888), (700, 8, 2100, 384), (260, 16, 2048, 128)]
+         (24, 128, 520, 2400), (2, 200, 520, 1888), (700, 8, 2100, 384), (260, 16, 2048, 128), (200, 64, 4200, 288),
+         (200, 64, 4200, 384), (300, 40, 8300, 1184), (70, 64, 4200, 1184), (100, 40, 9000, 288), (70, 16, 4200, 1536),
+         (33, 40, 1030, 256), (3, 300, 520, 416), (60, 700, 130, 160)]
 
 
 @pytest.mark.parametrize("mean,E,n,k", TILED)
@@ -342,6 +344,35 @@ def test_grouped_scales_at_any_address(ar, off, gather):
         want = ar.mxfp4_grouped_gemm_a4(xp, xs, wp, ws, o, rows=rows)
         assert torch.equal(ar.mxfp4_grouped_gemm_a4(xp, moved(xs), wp, moved(ws), o, rows=rows), want)
         assert torch.equal(ar.mxfp4_grouped_gemm(X.bfloat16(), wp, moved(ws), o, rows=rows), want)
+
+
+@pytest.mark.parametrize("borders", [[-5, 3, 2, 50, 7], [9, 9, 0, 0, 4], [2 ** 31 - 1, -2 ** 31, 5, 5, 2 ** 31 - 1],
+                                     [0, 1000, 0, 1000, 0], [40, 30, 20, 10, 0]])
+@pytest.mark.parametrize("m,n,k", [(10, 40, 96), (700, 1030, 288), (700, 1030, 256)])
+def test_grouped_cuts_borders_that_do_not_ascend(ar, borders, m, n, k):
+    # rows of experts whose borders are in order come out, whatever the others' are; nothing around Y is written
+    rng = np.random.default_rng(m)
+    wp, ws, W = _operand(rng, k, 4, n)
+    xp, xs, X = _operand(rng, k, m)
+    o = _dev(np.array(borders, np.int64).astype(np.int32))
+    cut = np.clip(np.array(borders, np.int64), 0, m)
+    spans = [(max(lo, 0), max(lo, hi)) for lo, hi in zip(cut[:-1], cut[1:])]
+    owners = np.zeros(m, int)
+    for lo, hi in spans:
+        owners[lo:hi] += 1
+    for a4 in (False, True):
+        buf = torch.full((m + 2, n), 7.0, device="cuda")
+        print(f"{borders} {m}x{n}x{k} a4 {a4}", flush=True)
+        if a4:
+            ar.mxfp4_grouped_gemm_a4(xp, xs, wp, ws, o, out=buf[1:-1])
+        else:
+            ar.mxfp4_grouped_gemm(X.bfloat16(), wp, ws, o, out=buf[1:-1])
+        assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+        assert (buf[1:-1][_dev(owners == 0)] == 7).all()
+        if sum(hi - lo for lo, hi in spans) <= m:      # no more tiles than borders in order can need
+            for e, (lo, hi) in enumerate(spans):
+                alone = _dev((owners == 1) & (np.arange(m) >= lo) & (np.arange(m) < hi))
+                assert torch.equal(buf[1:-1][alone], (X[alone] @ W[e].t()).float())
 
 
 def test_grouped_past_32_bit_offsets(ar):
@@ -576,9 +607,10 @@ def test_moe_of_packed_operators(ar, t):
         ref, written = moe.grouped(X, W, o["offsets"], rows, bias)
         mag, _ = moe.grouped(np.abs(X), np.abs(W), o["offsets"], rows, None if bias is None else np.abs(bias))
         assert written[:n].all() and not written[n:].any()
+        ref, mag, got = ref[:n], mag[:n], got[:n]
         tol = (K + 1) * U24 * mag
-        assert (np.abs(got - ref) <= tol + U8 * (np.abs(ref) + tol))[:n].all()
-    ref, mag = moe.combine(o["z"], o["pos"], o["weight"], o["r"])
+        assert (np.abs(got - ref) <= tol + U8 * (np.abs(ref) + tol)).all()
+    ref, mag = moe.combine(o["z"][:n], o["pos"], o["weight"], o["r"])
     tol = (2 * k + 1) * U24 * mag
     assert (np.abs(o["y"] - ref) <= tol + U8 * (np.abs(ref) + tol)).all()
 
