@@ -21,7 +21,7 @@ namespace ar {
 //   16384 x 128 x 2048 x 4096 (128): 64x256 384, 64x128 373, 256x256 385
 //   3000 x 16 x 4096 x 2080 (188): 128x128 69, 64x128 74, 256x256 98
 //   32768 x 128 x 4096 x 2048 (256): 256x256 584, 64x256 652, 128x128 686
-//   4096 x 8 x 11008 x 4096 (512): 128x128 358, 128x256 359, 256x256 367
+//   4096 x 8 x 11008 x 4096 (512): 256x256 367, 128x128 358; gathered from 2048 tokens, with bias and SiLU 382 and 402
 //   32768 x 32 x 4096 x 4096 (1024): 256x256 926, 128x256 1040, 128x128 1081
 hipError_t launch_mx_grouped_a16(const MxGroupArgs& a, hipStream_t stream) {
     const int64_t mean = a.M / a.E;
@@ -31,7 +31,7 @@ hipError_t launch_mx_grouped_a16(const MxGroupArgs& a, hipStream_t stream) {
         if (likely_tiles(a, 64, 256) > 1024) launch_groups<false, 64, 256, 1, 4, 1, 2, 3, 2>(a, stream);
         else launch_groups<false, 64, 128, 2, 2, 1, 4, 3, 2>(a, stream);
     } else {
-        if (likely_tiles(a, 256, 256) > 1024) launch_groups<false, 256, 256, 2, 4, 1, 2, 3>(a, stream);
+        if (likely_tiles(a, 256, 256) > 768) launch_groups<false, 256, 256, 2, 4, 1, 2, 3>(a, stream);
         else launch_groups<false, 128, 128, 2, 2, 1, 2, 3, 2>(a, stream);
     }
     return hipGetLastError();

@@ -27,6 +27,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// A barrier after this wavefront's LDS accesses that, other than
+// __syncthreads(), does not wait for its global loads and stores.
+__device__ __forceinline__ void lds_written_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 template <bool BF16>
 __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
     if constexpr (BF16) static_cast<uint16_t*>(y)[i] = (uint16_t)pack_bf16x2(v, v);
@@ -78,16 +82,16 @@ template <bool BF16>
 __device__ __forceinline__ float mx_gate(float v, float u) {
     if constexpr (BF16) {
         const float h = __builtin_amdgcn_exp2f(-0.72134752f * fabsf(u)), s = u < 0.0f ? h : 1.0f;
-        return (v * s) * (s * __builtin_amdgcn_rcpf(1.0f + h * h));
+        return (v * s) * (s * __builtin_amdgcn_rcpf(__builtin_fmaf(h, h, 1.0f)));
     } else {
         const float h = expf(-0.5f * fabsf(u)), s = u < 0.0f ? h : 1.0f;
-        return (v * s) * (s / (1.0f + h * h));
+        return (v * s) * (s / __builtin_fmaf(h, h, 1.0f));
     }
 }
 
 template <bool BF16>
 __device__ __forceinline__ float mx_gelu(float v) {
-    const float d = 1.0f + 0.35355339f * fabsf(v), w = 0.25f * (v * v);   // h = exp(-z^2 / 2)
+    const float d = __builtin_fmaf(0.35355339f, fabsf(v), 1.0f), w = 0.25f * (v * v);   // h = exp(-z^2 / 2)
     const float t = BF16 ? __builtin_amdgcn_rcpf(d) : 1.0f / d;
     const float h = BF16 ? __builtin_amdgcn_exp2f(-1.44269504f * w) : expf(-w);
     constexpr float P[11] = {0.282094806f,   0.282093763f, 0.24688457f,  0.175315976f,  0.0934624374f, -0.0592113584f,
@@ -103,7 +107,7 @@ template <bool BF16, int ACT>
 __device__ __forceinline__ float mx_act(float v) {
     if constexpr (ACT == kMxRelu) return v < 0.0f ? 0.0f : v;   // NaN stays
     else if constexpr (ACT == kMxSilu) return mx_gate<BF16>(v, v);
-    else if constexpr (ACT == kMxGeluTanh) return mx_gate<BF16>(v, v * (1.5957691216f + 0.0713548163f * (v * v)));
+    else if constexpr (ACT == kMxGeluTanh) return mx_gate<BF16>(v, v * __builtin_fmaf(0.0713548163f, v * v, 1.5957691216f));
     else if constexpr (ACT == kMxGelu) return mx_gelu<BF16>(v);
     else return v;
 }
@@ -487,22 +491,34 @@ __device__ __forceinline__ f32x16 mx_apart(f32x16 block) {
 
 // The same with an epilogue: a wavefront passes 32 rows of its blocks at a time
 // through its own part of LDS (`lds`, 128 TN * 32 bytes), so that a lane has four
-// neighbouring columns and a row of 64 is written in one piece, U steps of rows
-// at a time with the next ones' residual on their way.  One branch for the
-// activation ahead of all, then loops whose code is there once: unrolled over
+// neighbouring columns and a row of 64 is written in one piece.  The residual of
+// AHEAD steps of rows is on its way while those before are worked on (with the
+// loads of four steps waited for together, 4096 x 28672 x 8192 packed took 609 us,
+// without a residual 455).  One branch for the
+// activation ahead of all, then a loop whose code is there once: unrolled over
 // the blocks the code outgrows the instruction cache, and a 256x256 tile spent
 // 8 to 17 us here.
-template <int TM, int TN, bool BF16, class Args>
+template <int TM, int TN, bool BF16, int AHEAD, class Args>
 __device__ __forceinline__ void finish_tile(const f32x16 (&acc)[TM][TN], const Args& a, float* lds, int64_t m0, int64_t m1,
                                             int64_t n0, int64_t brow) {
-    constexpr int WN = 32 * TN, LPR = WN / 4, RPS = 64 / LPR, STEPS = 32 / RPS, U = 4;   // lanes a row, rows a step, steps
+    constexpr int WN = 32 * TN, LPR = WN / 4, RPS = 64 / LPR, STEPS = 32 / RPS;   // lanes a row, rows a step, steps
     constexpr int64_t ES = BF16 ? 2 : 4;
-    static_assert(STEPS % U == 0, "whole turns of the loop");
     const int lane = threadIdx.x & 63, half = lane >> 5, r = lane & 31, row = lane / LPR, col = lane % LPR * 4;
     const int64_t n = n0 + col, left = a.N - n;
     const int tile_rows = (int)max(min(m1 - m0, (int64_t)TM * 32), (int64_t)0);   // the wavefront's
     const int rows = left > 0 ? tile_rows - row : 0;                              // from this lane's first on
     const int64_t r_size = a.res_bf16 ? 2 : 4, y_step = RPS * a.ldy * ES, r_step = RPS * a.ldr * r_size;
+    const char* res_at = static_cast<const char*>(a.res) + ((m0 + row) * a.ldr + n) * r_size;
+    constexpr int U = 4;   // steps at a time, for registers' sake
+    static_assert(STEPS % U == 0 && STEPS % AHEAD == 0, "whole turns");
+    MxFour res[AHEAD];
+    if (a.res) {
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) {
+            if (s * RPS < rows) res[s].load(res_at, a.res_bf16, a.wide, left);
+            res_at += r_step;
+        }
+    }
     f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
     if (a.bias && left > 0) {
         MxFour b;
@@ -512,22 +528,10 @@ __device__ __forceinline__ void finish_tile(const f32x16 (&acc)[TM][TN], const A
     // The halves of a wavefront write rows four apart, which meet in the same banks of LDS: a row whose number has bit 2
     // set holds its columns 32 places on (64 columns), so that they do not.  Step s reads rows RPS s + row.
     constexpr int TURN = TN == 2 ? 32 : 0;
-    static_assert(TN != 2 || (RPS == 4 && U % 2 == 0), "bit 2 of a step's rows is the step's parity");
+    static_assert(TN != 2 || RPS == 4, "bit 2 of a step's rows is the step's parity");
     const float *from = lds + row * WN + col, *from_odd = lds + row * WN + (col ^ TURN);
     mx_with_act(a.act, [&](auto Act) {
         char* y = static_cast<char*>(a.y) + ((m0 + row) * a.ldy + n) * ES;
-        const char* res = static_cast<const char*>(a.res) + ((m0 + row) * a.ldr + n) * r_size;
-        MxFour now[U], next[U];
-        auto ahead = [&](int done) __attribute__((always_inline)) {   // rows done + RPS q
-            if (a.res) {
-#pragma unroll
-                for (int q = 0; q < U; ++q) {
-                    if (done + q * RPS < rows) next[q].load(res, a.res_bf16, a.wide, left);
-                    res += r_step;
-                }
-            }
-        };
-        ahead(0);
 #pragma nounroll
         for (int i = 0; i < TM; ++i) {
             if (i * 32 >= tile_rows) break;
@@ -544,25 +548,28 @@ __device__ __forceinline__ void finish_tile(const f32x16 (&acc)[TM][TN], const A
                 }
             });
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma nounroll
-            for (int s = 0; s < STEPS; s += U) {
-                const int done = i * 32 + s * RPS;
-#pragma unroll
-                for (int q = 0; q < U; ++q) now[q] = next[q];
-                ahead(done + U * RPS);
+            gemm::static_for<STEPS / U>([&](auto G) {
+                constexpr int s0 = decltype(G)::value * U;
                 f32x4 v[U];
 #pragma unroll
-                for (int q = 0; q < U; ++q) v[q] = *reinterpret_cast<const f32x4*>((q & 1 ? from_odd : from) + (s + q) * RPS * WN);
+                for (int q = 0; q < U; ++q)
+                    v[q] = *reinterpret_cast<const f32x4*>(((s0 + q) & 1 ? from_odd : from) + (s0 + q) * RPS * WN);
 #pragma unroll
                 for (int q = 0; q < U; ++q) {
+                    const int first = i * 32 + (s0 + q) * RPS;
                     v[q] += bias;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[q][k] = mx_act<BF16, decltype(Act)::value>(v[q][k]);
-                    if (a.res) v[q] += now[q].get(a.res_bf16, a.wide);
-                    if (done + q * RPS < rows) mx_store_four<BF16, true>(y, v[q], a.wide, left);
+                    if (a.res) {
+                        MxFour& mine = res[(s0 + q) % AHEAD];
+                        v[q] += mine.get(a.res_bf16, a.wide);
+                        if (first + AHEAD * RPS < rows) mine.load(res_at, a.res_bf16, a.wide, left);
+                        res_at += r_step;
+                    }
+                    if (first < rows) mx_store_four<BF16, true>(y, v[q], a.wide, left);
                     y += y_step;
                 }
-            }
+            });
         }
     });
 }
@@ -770,8 +777,8 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(Args a)
         constexpr int PER = sizeof(sw0) / (32 * WN * 4);   // wavefronts in one of the buffers of W
         static_assert(2 * PER >= NW, "32 rows of every wavefront");
         char* at = (wave < PER ? sw0 : sw1) + wave % PER * (32 * WN * 4);
-        finish_tile<TM, TN, BF16>(acc, a, reinterpret_cast<float*>(at), m0 + wm * WM, m1, n0 + wn * WN,
-                                  (int64_t)spot.e * a.N);
+        finish_tile<TM, TN, BF16, TN == 1 ? 4 : 8>(acc, a, reinterpret_cast<float*>(at), m0 + wm * WM, m1, n0 + wn * WN,
+                                                   (int64_t)spot.e * a.N);
     } else {
         store_tile<TM, TN, BF16>(acc, a, m0, n0, wm * WM, wn * WN);
     }
@@ -1093,8 +1100,8 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
         constexpr int PER = STAGE / (32 * WN * 4);   // wavefronts in a stage
         static_assert(3 * PER >= NW, "32 rows of every wavefront");
         char* at = (wave < PER ? st0 : wave < 2 * PER ? st1 : st2) + wave % PER * (32 * WN * 4);
-        finish_tile<TM, TN, BF16>(acc, a, reinterpret_cast<float*>(at), m0 + wm * WM, m1, n0 + wn * WN,
-                                  (int64_t)spot.e * a.N);
+        finish_tile<TM, TN, BF16, MINW >= 4 || TN == 1 ? 4 : 8>(acc, a, reinterpret_cast<float*>(at), m0 + wm * WM, m1,
+                                                                n0 + wn * WN, (int64_t)spot.e * a.N);
         return;
     }
     // Half a block at a time through LDS: every set's sums, then all threads add
@@ -1114,49 +1121,52 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
         for (int w = 1; w < NWK; ++w) v += *reinterpret_cast<const f32x4*>(red + ((set * NWK + w) * 16 + row) * 36 + c);
         return v;
     };
-    if constexpr (kMxEpilogue<Args>) {   // one branch for the activation, then code that is there once, as in finish_tile
+    if constexpr (kMxEpilogue<Args>) {   // bias and residual first, all of them on their way; then one branch for the activation
         const int64_t brow = (int64_t)spot.e * a.N;
-        mx_with_act(a.act, [&](auto Act) {
-            constexpr int UNROLL = 2 * TM * TN <= 4 ? 4 : 1;
-#pragma unroll UNROLL
-            for (int b = 0; b < 2 * TM * TN; ++b) {
-                const int h = b & 1, i = (b >> 1) / TN, j = (b >> 1) % TN;
-                MxFour bias[PER], res[PER];   // on their way during the barriers
-                int64_t m[PER], n[PER];
+        const int64_t b_size = a.bias_bf16 ? 2 : 4, r_size = a.res_bf16 ? 2 : 4;
+        constexpr int HALVES = 2 * TM * TN;
+        MxFour bias[PER][TN], res[PER][HALVES];
+        int64_t m[PER], n[PER];   // this lane's row and columns of the first half; m is past any row where there are none
 #pragma unroll
-                for (int q = 0; q < PER; ++q) {
-                    const int t = (q * NWK + wk) * 64 + lane;
-                    m[q] = m0 + wm * WM + i * 32 + h * 16 + (t >> 3);
-                    n[q] = n0 + wn * WN + j * 32 + (t & 7) * 4;
-                    if (t >> 3 >= 16 || n[q] >= a.N) m[q] = m1;   // nothing of this lane's
-                    if (m[q] < m1) {
-                        if (a.bias)
-                            bias[q].load(static_cast<const char*>(a.bias) + (brow + n[q]) * (a.bias_bf16 ? 2 : 4), a.bias_bf16,
-                                         a.wide, a.N - n[q]);
-                        if (a.res)
-                            res[q].load(static_cast<const char*>(a.res) + (m[q] * a.ldr + n[q]) * (a.res_bf16 ? 2 : 4),
-                                        a.res_bf16, a.wide, a.N - n[q]);
-                    }
-                }
-                __syncthreads();
-                gemm::static_for<2 * TM * TN>([&](auto B) {
-                    constexpr int p = decltype(B)::value;
-                    if (b == p) put(mx_apart<p>(acc[p / 2 / TN][p / 2 % TN]), 8 * (p % 2));
-                });
-                __syncthreads();
+        for (int q = 0; q < PER; ++q) {
+            const int t = (q * NWK + wk) * 64 + lane;
+            m[q] = t >> 3 < 16 ? m0 + wm * WM + (t >> 3) : m1;
+            n[q] = n0 + wn * WN + (t & 7) * 4;
+            if (a.bias) {
 #pragma unroll
-                for (int q = 0; q < PER; ++q) {
-                    const int t = (q * NWK + wk) * 64 + lane;
-                    if (m[q] >= m1) continue;
-                    f32x4 v = sums(t >> 3, (t & 7) * 4);
-                    if (a.bias) v += bias[q].get(a.bias_bf16, a.wide);
+                for (int j = 0; j < TN; ++j)
+                    if (n[q] + j * 32 < a.N)
+                        bias[q][j].load(static_cast<const char*>(a.bias) + (brow + n[q] + j * 32) * b_size, a.bias_bf16, a.wide,
+                                        a.N - n[q] - j * 32);
+            }
+            if (a.res) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = mx_act<BF16, decltype(Act)::value>(v[k]);
-                    if (a.res) v += res[q].get(a.res_bf16, a.wide);
-                    mx_store_four<BF16, false>(static_cast<char*>(a.y) + (m[q] * a.ldy + n[q]) * (BF16 ? 2 : 4), v, a.wide,
-                                               a.N - n[q]);
+                for (int b = 0; b < HALVES; ++b) {
+                    const int64_t mb = m[q] + b / 2 / TN * 32 + b % 2 * 16, nb = n[q] + b / 2 % TN * 32;
+                    if (mb < m1 && nb < a.N)
+                        res[q][b].load(static_cast<const char*>(a.res) + (mb * a.ldr + nb) * r_size, a.res_bf16, a.wide, a.N - nb);
                 }
             }
+        }
+        mx_with_act(a.act, [&](auto Act) {
+            gemm::static_for<HALVES>([&](auto B) {
+                constexpr int b = decltype(B)::value, j = b / 2 % TN;
+                lds_written_barrier();
+                put(acc[b / 2 / TN][j], 8 * (b % 2));
+                lds_written_barrier();
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    const int t = (q * NWK + wk) * 64 + lane;
+                    const int64_t mb = m[q] + b / 2 / TN * 32 + b % 2 * 16, nb = n[q] + j * 32;
+                    if (mb >= m1 || nb >= a.N) continue;
+                    f32x4 v = sums(t >> 3, (t & 7) * 4);
+                    if (a.bias) v += bias[q][j].get(a.bias_bf16, a.wide);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = mx_act<BF16, decltype(Act)::value>(v[k]);
+                    if (a.res) v += res[q][b].get(a.res_bf16, a.wide);
+                    mx_store_four<BF16, false>(static_cast<char*>(a.y) + (mb * a.ldy + nb) * (BF16 ? 2 : 4), v, a.wide, a.N - nb);
+                }
+            });
         });
         return;
     }
