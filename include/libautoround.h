@@ -368,8 +368,8 @@ AR_API ar_status ar_moe_route(const void* logits, ar_dtype lt, int64_t T, int32_
  *            yt.  Y may be the residual itself (same pointer and dtype)
  * T = 0 is an empty problem.  Errors: AR_ERR_INVALID_ARG for a NULL pointer,
  * P < 0, N < 1, T < 0, k < 1, an unknown dtype or an output that overlaps an
- * input; AR_ERR_UNSUPPORTED for k > 64, T k > 2^24, more than 2^34 elements or
- * a pointer that is not aligned as its type.  Nothing is allocated;
+ * input; AR_ERR_UNSUPPORTED for k > 64, T k > 2^24, N >= 2^31, more than 2^34
+ * elements or a pointer that is not aligned as its type.  Nothing is allocated;
  * stream-ordered, no synchronization. */
 AR_API ar_status ar_moe_combine(const void* Z, ar_dtype zt, int64_t P, int64_t N, const int32_t* pos, const float* weight,
                          int64_t T, int32_t k, const void* residual, ar_dtype residual_dtype, void* Y, ar_dtype yt,

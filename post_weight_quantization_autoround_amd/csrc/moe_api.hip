@@ -46,6 +46,7 @@ ar_status ar_moe_combine(const void* Z, ar_dtype zt, int64_t P, int64_t N, const
     if (T > kMoeMaxSlots / k) return fail(AR_ERR_UNSUPPORTED, "at most %lld choices in all", (long long)kMoeMaxSlots);
     if (P > INT32_MAX || (P > 0 && N > kMaxElems / P) || (T > 0 && N > kMaxElems / T) || N > kMaxElems)
         return fail(AR_ERR_UNSUPPORTED, "problem too large");
+    if (N >= (int64_t)1 << 31) return fail(AR_ERR_UNSUPPORTED, "N must be below 2^31");   // a launch holds a token
     if (!dtype_ok(zt) || !dtype_ok(yt)) return fail(AR_ERR_INVALID_ARG, "unknown Z or Y dtype");
     if (residual && !dtype_ok(residual_dtype)) return fail(AR_ERR_INVALID_ARG, "unknown residual dtype");
     if (T == 0) return AR_OK;

@@ -533,13 +533,26 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(MoeCombineArgs a, uint
 }
 
 template <int C>
-void launch_combine(const MoeCombineArgs& a, hipStream_t stream) {
-    const uint32_t blocks_n = (uint32_t)((a.N + 256 * C - 1) / (256 * C));
-    const dim3 grid((unsigned)(a.T * blocks_n)), block(256);
-    if (a.z_bf16 && a.y_bf16) hipLaunchKernelGGL((moe_combine_kernel<C, true, true>), grid, block, 0, stream, a, blocks_n);
-    else if (a.z_bf16) hipLaunchKernelGGL((moe_combine_kernel<C, true, false>), grid, block, 0, stream, a, blocks_n);
-    else if (a.y_bf16) hipLaunchKernelGGL((moe_combine_kernel<C, false, true>), grid, block, 0, stream, a, blocks_n);
-    else hipLaunchKernelGGL((moe_combine_kernel<C, false, false>), grid, block, 0, stream, a, blocks_n);
+hipError_t launch_combine(const MoeCombineArgs& all, hipStream_t stream) {
+    const uint32_t blocks_n = (uint32_t)((all.N + 256 * C - 1) / (256 * C));   // (N below 2^31: at most 2^23)
+    // tokens that one launch's fewer than 2^32 threads hold; the others go to further launches
+    const int64_t most = ((1 << 24) - 1) / blocks_n;
+    for (int64_t t0 = 0; t0 < all.T; t0 += most) {
+        MoeCombineArgs a = all;
+        a.T = all.T - t0 < most ? all.T - t0 : most;
+        a.pos += t0 * a.k;
+        a.weight += t0 * a.k;
+        if (a.res) a.res = static_cast<const char*>(a.res) + t0 * a.N * (a.res_bf16 ? 2 : 4);
+        a.y = static_cast<char*>(a.y) + t0 * a.N * (a.y_bf16 ? 2 : 4);
+        const dim3 grid((unsigned)(a.T * blocks_n)), block(256);
+        if (a.z_bf16 && a.y_bf16) hipLaunchKernelGGL((moe_combine_kernel<C, true, true>), grid, block, 0, stream, a, blocks_n);
+        else if (a.z_bf16) hipLaunchKernelGGL((moe_combine_kernel<C, true, false>), grid, block, 0, stream, a, blocks_n);
+        else if (a.y_bf16) hipLaunchKernelGGL((moe_combine_kernel<C, false, true>), grid, block, 0, stream, a, blocks_n);
+        else hipLaunchKernelGGL((moe_combine_kernel<C, false, false>), grid, block, 0, stream, a, blocks_n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
@@ -586,9 +599,7 @@ hipError_t launch_moe_combine(const MoeCombineArgs& a, hipStream_t stream) {
         auto ok = [](const void* p, bool bf16) { return reinterpret_cast<uintptr_t>(p) % (bf16 ? 8 : 16) == 0; };
         return ok(a.z, a.z_bf16) && ok(a.res, a.res_bf16) && ok(a.y, a.y_bf16);
     }();
-    if (four) launch_combine<4>(a, stream);
-    else launch_combine<1>(a, stream);
-    return hipGetLastError();
+    return four ? launch_combine<4>(a, stream) : launch_combine<1>(a, stream);
 }
 
 }  // namespace ar

@@ -539,8 +539,9 @@ def test_combine_carries_nan_and_infinity(ar):
     assert (ar.moe_combine(Z[:0], pos, w) == 0).all()
 
 
-def test_combine_past_32_bit_offsets(ar):
-    t, n, k = 140_000, 32_000, 2
+@pytest.mark.parametrize("n", [32_000, 32_001])           # in pieces of four columns and of one
+def test_combine_past_32_bit_offsets(ar, n):
+    t, k = 140_000, 2
     Z = torch.zeros(t, n, dtype=torch.bfloat16, device="cuda")
     rows = [0, 67_108, 134_218, t - 1]
     part = _exact(np.random.default_rng(4), len(rows), n)
@@ -665,6 +666,30 @@ def test_captured_graph_and_other_streams(ar, t):
         for n in o:
             if n != "z":      # rows of z behind the last are not written
                 assert torch.equal(o[n], want[n]), n
+    del graph
+
+
+def test_captured_route_of_many_slots(ar):
+    # the form that keeps its counts in pos meanwhile, captured; replays with other scores, each against an eager call
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x, b = torch.empty(7000, 48, device="cuda"), torch.zeros(48, device="cuda")
+    ar.moe_route(x.zero_(), 3)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ar.moe_route(x, 3, score="sigmoid", bias=b)
+    for rep in range(4):
+        x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+        b.copy_(0.2 * torch.randn(48, generator=gen, device="cuda"))
+        if rep == 2:
+            x[:6990] = -float("inf")
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        first = [g.clone() for g in got]
+        for g, w in zip(first, ar.moe_route(x, 3, score="sigmoid", bias=b)):
+            assert torch.equal(g, w), rep
+        assert int(first[2][-1]) == (30 if rep == 2 else 21000)
     del graph
 
 

@@ -85,7 +85,7 @@ CASES = ([(n, kw, e) for n in ("ar_mxfp4_linear", "ar_mxfp4_linear_a4") for kw, 
     ("ar_moe_combine", dict(k=0), INVALID), ("ar_moe_combine", dict(k=65), UNSUPPORTED),
     ("ar_moe_combine", dict(zt=2), INVALID), ("ar_moe_combine", dict(yt=2), INVALID), ("ar_moe_combine", dict(rt=2), INVALID),
     ("ar_moe_combine", dict(T=(1 << 23) + 1), UNSUPPORTED), ("ar_moe_combine", dict(P=1 << 31), UNSUPPORTED),
-    ("ar_moe_combine", dict(N=(1 << 33)), UNSUPPORTED),
+    ("ar_moe_combine", dict(N=(1 << 33)), UNSUPPORTED), ("ar_moe_combine", dict(N=1 << 31, T=1, P=1), UNSUPPORTED),
     *[("ar_moe_combine", {p: None}, INVALID) for p in ("Z", "pos", "weight", "Y")],
     *[("ar_moe_combine", {p: 0x10002 + 0x10000 * i}, UNSUPPORTED)
       for i, p in enumerate(("Z", "pos", "weight", "residual", "Y"))],
