@@ -432,6 +432,11 @@ def _named(table, name, what):
         raise ValueError(f"{what} must be one of {', '.join(table)}, got {name!r}") from None
 
 
+def _i32(n):
+    # a count for a 32-bit argument: one that needs more bits arrives as one that the library refuses
+    return max(min(int(n), 2 ** 31 - 1), -1)
+
+
 def _row_stride(t):
     # the stride of a lone row means nothing
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
@@ -503,7 +508,7 @@ def _mx_grouped(call, x_rows, K, x, packed, scale, offsets, rows, bias, act, out
     code = _named(ACTIVATIONS, act, "act")
     pb, bt = (None, 0) if bias is None else (_mx_in(bias, "bias", _F32_BF16, dev, (E, N)), _dtype_code(bias))
     out = _mx_y(out, out_dtype, M, N, like, dev)
-    _check(call(*x, x_rows, K, pr, pp, ps, E, N, po, pb, bt, code, out.data_ptr(), _dtype_code(out), M,
+    _check(call(*x, x_rows, K, pr, pp, ps, _i32(E), N, po, pb, bt, code, out.data_ptr(), _dtype_code(out), M,
                 _mx_stream(dev)))
     return out
 
@@ -550,13 +555,13 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", normalize: b
     T, E = logits.shape
     pb = None if bias is None else _mx_in(bias, "bias", _F32, dev, (E,))
     how = _named(SCORES, score, "score")
-    k = int(k)
-    n = max(k, 0)
+    k = _i32(k)
+    n = max(min(k, E), 0)
     expert, pos = (logits.new_empty((T, n), dtype=torch.int32) for _ in range(2))
     weight = logits.new_empty((T, n), dtype=torch.float32)
     offsets = logits.new_empty(E + 1, dtype=torch.int32)
     token = logits.new_empty(T * n, dtype=torch.int32)
-    _check(lib.ar_moe_route(pl, _dtype_code(logits), T, E, k, how, pb, int(normalize), weight_scale, expert.data_ptr(),
+    _check(lib.ar_moe_route(pl, _dtype_code(logits), T, _i32(E), k, how, pb, int(normalize), weight_scale, expert.data_ptr(),
                             weight.data_ptr(), offsets.data_ptr(), token.data_ptr(), pos.data_ptr(), _mx_stream(dev)))
     return expert, weight, offsets, token, pos
 
@@ -577,7 +582,7 @@ def moe_combine(Z: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor, residu
     if residual is not None:
         pr, rt = _mx_in(residual, "residual", _F32_BF16, dev, (T, N)), _dtype_code(residual)
     out = _mx_y(out, out_dtype, T, N, Z, dev)
-    _check(lib.ar_moe_combine(pz, _dtype_code(Z), P, N, pp, pw, T, k, pr, rt, out.data_ptr(), _dtype_code(out),
+    _check(lib.ar_moe_combine(pz, _dtype_code(Z), P, N, pp, pw, T, _i32(k), pr, rt, out.data_ptr(), _dtype_code(out),
                               _mx_stream(dev)))
     return out
 

@@ -429,9 +429,10 @@ struct Mover {
         }
     }
     // the same with row r of the tile being row at(r) of the `rows` at `base` (below 2^31 bytes in all), zeros for -1
+    // (one row at least: the stage offset is taken off the buffer's size, and would wrap around a size of 0)
     template <class At>
     __device__ __forceinline__ void gather(const void* base, int64_t rows, int64_t pitch, int w, At at) {
-        init(base, 0, rows, pitch, w);
+        init(base, 0, rows > 0 ? rows : 1, pitch, w);
         const int lane = threadIdx.x & 63;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {

@@ -298,6 +298,35 @@ def test_grouped_exact_over_the_tiles(ar, mean, E, n, k, gather):
         assert torch.equal(ar.mxfp4_grouped_gemm_a4(xp, xs, wp, ws, o, **more)[:-3], want)
 
 
+# packed X in the tile kernels (K a multiple of 128) of 64, 128 and 256 rows, and both forms in the ring's gathered loads
+@pytest.mark.parametrize("mean,E,n,k", [(8, 200, 520, 512), (100, 40, 4100, 640), (300, 16, 4200, 1024), (70, 64, 2048, 416)])
+@pytest.mark.parametrize("real_rows", [0, 1, 100])
+def test_grouped_rows_that_do_not_exist(ar, mean, E, n, k, real_rows):
+    rng = np.random.default_rng(mean + E + n + k + real_rows)
+    m = mean * E
+    offsets = np.concatenate([[0], np.cumsum(rng.multinomial(m, rng.dirichlet(np.full(E, 2.0))))]).astype(np.int32)
+    rows = rng.integers(-2, real_rows + 2, m).astype(np.int32)
+    rows[::7] = rng.choice([-1, real_rows, -2 ** 31, 2 ** 31 - 1], len(rows[::7]))
+    wp, ws, W = _operand(rng, k, E, n)
+    xp, xs, X = _operand(rng, k, 100)
+    xp, xs, X = xp[:real_rows], xs[:real_rows], X[:real_rows]
+    bias = _exact(rng, E, n)
+    zero = torch.cat((X, torch.zeros((1, k), dtype=X.dtype, device="cuda")))
+    r = torch.from_numpy(rows.astype(np.int64))
+    r[(r < 0) | (r >= real_rows)] = real_rows
+    want = torch.empty((m, n), dtype=torch.float64, device="cuda")
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        want[lo:hi] = zero[r[lo:hi].cuda()] @ W[e].t() + bias[e]
+    more = dict(rows=_dev(rows), bias=bias.float())
+    for a4 in (True, False):
+        print(f"{mean} rows x {E} x {n} x {k} of {real_rows} rows a4 {a4}", flush=True)
+        Y = ar.mxfp4_grouped_gemm_a4(xp, xs, wp, ws, _dev(offsets), **more) if a4 else \
+            ar.mxfp4_grouped_gemm(X.bfloat16(), wp, ws, _dev(offsets), **more)
+        assert torch.equal(Y, want.float())
+
+
+
 @pytest.mark.parametrize("mean,E,n,k", [(3, 6, 140, 96), (70, 4, 300, 416), (300, 4, 520, 288), (600, 4, 1030, 512)])
 def test_grouped_keeps_experts_apart(ar, mean, E, n, k):
     # every second expert's weight and every second token are NaN throughout; the others are untouched by them
@@ -724,6 +753,8 @@ def test_binding_refusals(ar):
         (lambda: ar.moe_route(lg, 0), ar.ARError),
         (lambda: ar.moe_route(lg, -1), ar.ARError),
         (lambda: ar.moe_route(lg, 9), ar.ARError),
+        (lambda: ar.moe_route(lg, 2 ** 32 + 2), ar.ARError),   # 2 in 32 bits
+        (lambda: ar.moe_route(lg, 2 - 2 ** 32), ar.ARError),
         (lambda: ar.moe_route(lg, 2, score="max"), ValueError),
         (lambda: ar.moe_route(lg, 2, bias=torch.zeros(4, device="cuda")), ValueError),
         (lambda: ar.moe_route(lg.half(), 2), TypeError),
