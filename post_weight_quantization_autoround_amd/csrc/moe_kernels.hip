@@ -468,7 +468,11 @@ __global__ void __launch_bounds__(kOrderThreads) moe_few_kernel(MoeRouteArgs a) 
 
 // ------------------------------------------------------------- combine -----
 // y[t, n] = res[t, n] + sum_j weight[t, j] z[pos[t, j], n], j ascending, in
-// fp32 with one rounding at the end.  A thread has C neighbouring columns.
+// fp32 with one rounding at the end.  A thread has C neighbouring columns: four,
+// 8 bytes of bf16, where all operands are aligned for it, else one.  Every row of
+// z is read once and y written once, which bounds it: 4096 tokens of 8 experts,
+// 4100 wide, bf16 to fp32, 67 us (4.6 TB/s).  A thread that goes on to further
+// columns or tokens in a loop is slower (101 us), so a workgroup has one piece.
 template <int C, bool BF16>
 __device__ __forceinline__ void load_cols(float (&v)[C], const void* p, int64_t at) {
     if constexpr (C == 1) {

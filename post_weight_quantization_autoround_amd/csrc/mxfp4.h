@@ -1,4 +1,4 @@
-// Packed MXFP4: quantization (mxfp4_quant.hip) and products (mxfp4_gemm.hip).
+// Packed MXFP4: quantization (mxfp4_quant.hip) and products (mxfp4_tiles.h; mxfp4_gemm.hip, mxfp4_linear.hip, mxfp4_grouped_*.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -524,6 +524,26 @@ def test_route_of_no_tokens_and_of_many(ar):
     assert torch.equal(pos.reshape(-1)[slot[:real]], torch.arange(real, device="cuda", dtype=torch.int32))
 
 
+def test_route_at_its_limits(ar):
+    t, e, k = 1 << 18, 1024, 64                          # 2^24 slots, the most experts and choices
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(t, e, generator=gen, device="cuda").bfloat16()      # (ties in every token)
+    expert, weight, offsets, token, pos = ar.moe_route(x, k, score="sigmoid", normalize=False)
+    first = 0
+    for part in x.split(1 << 16):
+        want = torch.sort(part, dim=-1, descending=True, stable=True)
+        n = part.shape[0]
+        assert torch.equal(expert[first:first + n], want[1][:, :k].int())
+        # rounded once from 64 bits, where the exponential may be off by an ulp: half a step of the 24 bits
+        s = torch.sigmoid(want[0][:, :k].double())
+        assert ((weight[first:first + n].double() - s).abs() <= s * (2.0 ** -24 + 2.0 ** -50)).all()
+        first += n
+    group, slot = torch.sort(expert.reshape(-1), stable=True)
+    assert torch.equal(offsets, torch.searchsorted(group, torch.arange(e + 1, dtype=torch.int32, device="cuda")).int())
+    assert torch.equal(token, (slot // k).int())
+    assert torch.equal(pos.reshape(-1)[slot], torch.arange(t * k, device="cuda", dtype=torch.int32))
+
+
 # ----------------------------------------------------------------- combine
 @pytest.mark.parametrize("t,k,n", [(1, 1, 1), (1, 8, 4096), (3, 2, 33), (16, 6, 2052), (5, 64, 130), (7, 9, 4100),
                                    (300, 8, 520), (2000, 3, 1024)])
