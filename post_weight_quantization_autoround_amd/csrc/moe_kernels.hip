@@ -28,7 +28,7 @@ __device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((
 // where two of the k + 1 largest lie closer than twice what that may be off by
 // (or are not finite) is it formed again in 64 bits, so that scores which the
 // definition tells apart are never taken for equal: 16384 tokens of 256 experts
-// 35 -> 23 us.  The weights are formed in 64 bits: there are few of them.
+// 35 -> 22 us.  The weights are formed in 64 bits: there are few of them.
 __device__ __forceinline__ uint64_t order_key(double s) {
     if (s != s) return ~0ull;
     if (s == -__builtin_inf()) return 0;
@@ -91,7 +91,8 @@ __device__ __forceinline__ float wave_max_nan(float v) {
 // and its key; with `want_next` the (k + 1)-th key too, 0 if there is none.  Up to eight
 // scores a lane are sorted first (neighbours change places where the first is
 // the smaller, so equal ones keep their order), and the lane that wins moves
-// its list up.
+// its list up.  A round is 23 vector instructions, which is what bounds many
+// tokens (16384 tokens of 256 experts: about 1 us a round).  V is at most 16.
 template <int V, class Key>
 __device__ __forceinline__ int choose(Key (&key)[V], int k, Key& of, Key& next, bool want_next) {
     constexpr bool SORTED = V <= 8;
@@ -112,35 +113,43 @@ __device__ __forceinline__ int choose(Key (&key)[V], int k, Key& of, Key& next, 
                 place[v] = up ? q : p;
                 place[v + 1] = up ? p : q;
             }
-    int mine = -1;
-    of = next = 0;
-    for (int j = 0; j < k + (want_next ? 1 : 0); ++j) {
-        Key best = key[0];
-        int at = place[0];
+    uint32_t places = 0;   // sorted: four bits each
+    if constexpr (SORTED)
+#pragma unroll
+        for (int v = 0; v < V; ++v) places |= (uint32_t)place[v] << 4 * v;
+    auto best = [&](uint32_t& at) {
+        Key b = key[0];
+        at = places;
         if constexpr (!SORTED)
 #pragma unroll
-            for (int v = 1; v < V; ++v)
-                if (key[v] > best) { best = key[v]; at = v; }
-        const Key max = wave_max(best);
-        if (max == 0) break;
-        if (j == k) { next = max; break; }
-        const int owner = __builtin_ctzll(__ballot(best == max));
-        const int taken = __builtin_amdgcn_readlane(at, owner);
-        if (lane == owner) {
-            if constexpr (SORTED) {
-#pragma unroll
-                for (int v = 0; v + 1 < V; ++v) {
-                    key[v] = key[v + 1];
-                    place[v] = place[v + 1];
-                }
-                key[V - 1] = 0;
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) key[v] = v == taken ? 0 : key[v];
+            for (int v = 1; v < V; ++v) {
+                at = key[v] > b ? v : at;
+                b = key[v] > b ? key[v] : b;
             }
+        return b;
+    };
+    int mine = -1;
+    uint32_t at;
+    of = 0;
+    for (int j = 0; j < k; ++j) {
+        const Key b = best(at), max = wave_max(b);
+        if (max == 0) break;
+        const int owner = __builtin_ctzll(__ballot(b == max)), taken = __builtin_amdgcn_readlane((int)at, owner) & 15;
+        if constexpr (SORTED) {   // (by masks: the compiler makes a search of selects)
+            const Key won = lane == owner ? ~(Key)0 : 0;
+#pragma unroll
+            for (int v = 0; v + 1 < V; ++v) key[v] = (key[v + 1] & won) | (key[v] & ~won);
+            key[V - 1] &= ~won;
+            places >>= 4 & (uint32_t)won;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = lane == owner && v == taken ? 0 : key[v];
         }
-        if (lane == j) { mine = owner * V + taken; of = max; }
+        // (selects: as branches they send `of` through memory)
+        mine = lane == j ? owner * V + taken : mine;
+        of = lane == j ? max : of;
     }
+    next = want_next ? wave_max(best(at)) : 0;
     return mine;
 }
 
