@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(NWM * NWN * 64) mx_gemm_a4_tile_kernel(Args a)
     wait_vmcnt<0>();   // the last, unread loads into LDS
 
     if constexpr (kMxEpilogue<Args>) {
-        lds_barrier();   // every wavefront is done with the stages
+        lds_written_barrier();   // every wavefront has read the stages
         constexpr int PER = sizeof(sw0) / (32 * WN * 4);   // wavefronts in one of the buffers of W
         static_assert(2 * PER >= NW, "32 rows of every wavefront");
         char* at = (wave < PER ? sw0 : sw1) + wave % PER * (32 * WN * 4);
@@ -1106,7 +1106,7 @@ __global__ void __launch_bounds__(NWM * NWN * NWK * 64, MINW) mx_gemm_ring_kerne
     wait_vmcnt<0>();
 
     if constexpr (kMxEpilogue<Args> && NWK == 1) {
-        lds_barrier();   // every wavefront is done with the stages
+        lds_written_barrier();   // every wavefront has read the stages
         constexpr int PER = STAGE / (32 * WN * 4);   // wavefronts in a stage
         static_assert(3 * PER >= NW, "32 rows of every wavefront");
         char* at = (wave < PER ? st0 : wave < 2 * PER ? st1 : st2) + wave % PER * (32 * WN * 4);
