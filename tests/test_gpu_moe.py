@@ -66,6 +66,7 @@ SHAPES = [(1, 1, 32), (1, 16, 64), (2, 33, 96), (15, 17, 128), (12, 900, 736), (
           (65, 48, 1120), (130, 4200, 416), (130, 4200, 1024), (130, 9000, 288), (257, 511, 544), (300, 9000, 640),
           (300, 17000, 288), (520, 17000, 288), (520, 17000, 768), (600, 9000, 352), (1100, 8000, 1088),
           (2000, 8300, 160), (2000, 8300, 512)]
+SHAPES += [(512, 11008, 512), (600, 9000, 640), (513, 8196, 256)]      # packed X in the tile kernel's 128x256
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -122,6 +123,40 @@ def test_linear_strides_and_in_place(ar, m, n, out):
         assert torch.equal(view, want) and (buf[:, :left] == 5).all()
 
 
+# with the test above every kernel of both forms, the larger ones with columns in fours and not
+STRIDED = [(20, 17001, 96), (130, 4201, 384), (300, 4203, 384), (600, 9000, 384), (600, 9001, 512), (520, 17000, 384),
+           (520, 17001, 512), (2000, 8300, 160), (2000, 8301, 160)]
+
+
+@pytest.mark.parametrize("m,n,k", STRIDED)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_linear_strides_and_in_place_over_the_tiles(ar, m, n, k, out):
+    rng = np.random.default_rng(m + n + k)
+    wp, ws, W = _operand(rng, k, n)
+    xp, xs, X = _operand(rng, k, m)
+    bias, res = _exact(rng, n), _exact(rng, m, n)
+    want = (X @ W.t() + bias + res).float().to(DT[out])
+    calls = [lambda **kw: ar.mxfp4_linear(X.bfloat16(), wp, ws, bias=bias.bfloat16(), out_dtype=DT[out], **kw),
+             lambda **kw: ar.mxfp4_linear_a4(xp, xs, wp, ws, bias=bias.float(), out_dtype=DT[out], **kw)]
+    for call, (left, pad), rdt in itertools.product(calls, [(0, 0), (4, 4), (1, 2)], ["f32", "bf16"]):
+        rbuf = torch.full((m, left + n + pad), 3.0, dtype=DT[rdt], device="cuda")
+        rbuf[:, left:left + n] = res.to(DT[rdt])
+        buf = torch.full((m + 2, left + n + pad), 7.0, dtype=DT[out], device="cuda")
+        print(f"{m}x{n}x{k} {out} {left} {pad} {rdt}", flush=True)
+        call(residual=rbuf[:, left:left + n], out=buf[1:-1, left:left + n])
+        assert torch.equal(buf[1:-1, left:left + n], want)
+        buf[1:-1, left:left + n] = 7.0
+        assert (buf == 7).all()
+    for call, left in itertools.product(calls, [0, 1]):      # onto the residual itself
+        buf = torch.full((m + 2, left + n), 5.0, dtype=DT[out], device="cuda")
+        view = buf[1:-1, left:]
+        view.copy_(res)
+        assert call(residual=view, out=view) is view
+        assert torch.equal(view, want)
+        view[:] = 5
+        assert (buf == 5).all()
+
+
 ACTS = ["relu", "silu", "gelu", "gelu_tanh"]
 
 
@@ -170,6 +205,38 @@ def test_activations(ar, act, m, n, k):
             Y = ar.mxfp4_linear_a4(xp, xs, wp, ws, **more) if a4 else ar.mxfp4_linear(X.bfloat16(), wp, ws, **more)
             err = np.abs(_np(Y[some]).astype(F64) - want)
             assert (err <= tol).all(), (err / tol).max()
+
+
+def _act_bias(n):
+    return np.concatenate([np.linspace(-30, 8, n - 40), np.linspace(-110, 110, 20), 10.0 ** np.arange(-38, 2, 2)]).astype(F32)
+
+
+def _check_act(got, v, act, out):
+    """act(v) within what test_activations allows; v as the kernel rounds it."""
+    want = moe.activate(v, act)
+    tol = np.abs(want) * _act_bound(v, act, out) + (2.0 ** -133 if out == "bf16" else 2.0 ** -148)
+    err = np.abs(_np(got).astype(F64) - want)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+ACT_SHAPES = [(16, 9000, 160), (20, 17000, 96), (130, 4200, 160), (300, 4200, 160), (600, 9000, 384), (2000, 8300, 160)]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n,k", ACT_SHAPES)      # with the test above every kernel of both forms
+def test_activations_over_the_tiles(ar, act, m, n, k):
+    rng = np.random.default_rng(m)
+    wp, ws, W = _operand(rng, k, n)
+    xp, xs, X = _operand(rng, k, m)
+    xs[:], X = xs - 2, X / 4
+    some = np.unique(np.concatenate([[0, m - 1], rng.integers(0, m, 4)]))
+    bias = _act_bias(n)
+    v = ((X[some] @ W.t()).cpu().numpy().astype(F32) + bias).astype(F64)
+    for out, a4 in itertools.product(("f32", "bf16"), (False, True)):
+        print(f"{act} {m}x{n}x{k} {out} a4 {a4}", flush=True)
+        more = dict(bias=_dev(bias), act=act, out_dtype=DT[out])
+        Y = ar.mxfp4_linear_a4(xp, xs, wp, ws, **more) if a4 else ar.mxfp4_linear(X.bfloat16(), wp, ws, **more)
+        _check_act(Y[some], v, act, out)
 
 
 @pytest.mark.parametrize("act", ["none"] + ACTS)
@@ -325,6 +392,36 @@ def test_grouped_rows_that_do_not_exist(ar, mean, E, n, k, real_rows):
             ar.mxfp4_grouped_gemm(X.bfloat16(), wp, ws, _dev(offsets), **more)
         assert torch.equal(Y, want.float())
 
+
+
+# every kernel of both forms
+ACT_TILED = [(16, 8, 520, 288), (70, 16, 4200, 160), (300, 6, 9000, 416), (1100, 4, 9000, 288), (2, 200, 520, 160),
+             (200, 64, 520, 256), (24, 128, 520, 256), (260, 16, 2048, 256), (200, 64, 4200, 288), (70, 64, 4200, 160),
+             (100, 40, 520, 256), (40, 64, 1030, 160)]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("mean,E,n,k", ACT_TILED)
+def test_grouped_activations_over_the_tiles(ar, act, mean, E, n, k):
+    rng = np.random.default_rng(mean + E)
+    sizes = rng.multinomial(mean * E, rng.dirichlet(np.full(E, 2.0)))
+    offsets = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    m, R = mean * E, max(1, mean * E // 4)
+    rows = rng.integers(0, R, m).astype(np.int32)
+    wp, ws, W = _operand(rng, k, E, n)
+    xp, xs, X = _operand(rng, k, R)
+    xs[:], X = xs - 2, X / 4
+    bias = np.stack([np.roll(_act_bias(n), 7 * e) for e in range(E)])
+    some = np.unique(np.concatenate([[0, m - 1], rng.integers(0, m, 4)]))
+    expert = np.searchsorted(offsets, some, side="right") - 1
+    P = np.stack([(W[e] @ X[rows[p]]).cpu().numpy() for p, e in zip(some, expert)])
+    v = (P.astype(F32) + bias[expert]).astype(F64)
+    for out, a4 in itertools.product(("f32", "bf16"), (False, True)):
+        print(f"{act} {mean} rows x {E} x {n} x {k} {out} a4 {a4}", flush=True)
+        more = dict(rows=_dev(rows), bias=_dev(bias), act=act, out_dtype=DT[out])
+        Y = ar.mxfp4_grouped_gemm_a4(xp, xs, wp, ws, _dev(offsets), **more) if a4 else \
+            ar.mxfp4_grouped_gemm(X.bfloat16(), wp, ws, _dev(offsets), **more)
+        _check_act(Y[some], v, act, out)
 
 
 @pytest.mark.parametrize("mean,E,n,k", [(3, 6, 140, 96), (70, 4, 300, 416), (300, 4, 520, 288), (600, 4, 1030, 512)])
