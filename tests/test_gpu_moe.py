@@ -621,6 +621,38 @@ def test_route_of_no_tokens_and_of_many(ar):
     assert torch.equal(pos.reshape(-1)[slot[:real]], torch.arange(real, device="cuda", dtype=torch.int32))
 
 
+# more than 2^14 slots: the experts in 1 to 16 wavefronts, 1 to 16 segments of which share the chunks, evenly and not; chunks
+# of 1024 slots and of 2048
+@pytest.mark.parametrize("t,e,k", [(5501, 40, 3), (2801, 65, 6), (4200, 100, 5), (6203, 128, 3), (2600, 200, 7), (5001, 256, 8),
+                                   (10007, 256, 8), (2301, 300, 8), (3001, 512, 7), (20003, 512, 4), (2200, 513, 8),
+                                   (1400, 1024, 13), (140_007, 256, 4)])
+def test_route_order_of_many_slots(ar, t, e, k):
+    gen = torch.Generator(device="cuda").manual_seed(t + e)
+    x = torch.randn(t, e, generator=gen, device="cuda") + 1.5 * torch.randn(e, generator=gen, device="cuda")
+    x[3::11] = -float("inf")                               # tokens of no expert, and some of fewer than k
+    x[5::17, 2:] = -float("inf")
+    x[:, e // 2] = -float("inf")                           # an expert without rows
+    expert, weight, offsets, token, pos = ar.moe_route(x, k)
+    key, index = torch.sort(x, dim=-1, descending=True, stable=True)
+    want = torch.where(key[:, :k] > -float("inf"), index[:, :k], -1).int()
+    assert torch.equal(expert, want) and (weight[want < 0] == 0).all()
+    flat = torch.where(want < 0, e, want).reshape(-1)
+    group, slot = torch.sort(flat, stable=True)
+    real = int((group < e).sum())
+    assert real < t * k and torch.equal(offsets, torch.searchsorted(group, torch.arange(e + 1, device="cuda").int()).int())
+    assert torch.equal(token[:real], (slot[:real] // k).int()) and (token[real:] == -1).all()
+    assert torch.equal(pos.reshape(-1)[slot[:real]], torch.arange(real, device="cuda", dtype=torch.int32))
+    assert (pos[want < 0] == -1).all()
+
+
+@pytest.mark.parametrize("t,e,k", [(2801, 65, 6), (2100, 200, 8), (2301, 256, 8), (2801, 400, 6)])
+def test_route_of_many_slots_by_biased_scores(ar, t, e, k):
+    rng = np.random.default_rng(t + e)
+    x = 1.5 * rng.standard_normal((t, e))
+    x[2::9] = -np.inf
+    _check_route(ar, x, k, "f32", 0.1 * rng.standard_normal(e), score="sigmoid", weight_scale=2.5)
+
+
 def test_route_at_its_limits(ar):
     t, e, k = 1 << 18, 1024, 64                          # 2^24 slots, the most experts and choices
     gen = torch.Generator(device="cuda").manual_seed(2)
