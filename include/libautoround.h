@@ -334,8 +334,9 @@ typedef enum { AR_SCORE_SOFTMAX = 0, AR_SCORE_SIGMOID = 1 } ar_score;
  * tokens, and the T k slots s = t k + j sorted by expert.
  * With s_e the softmax or the sigmoid of a token's logits, the choice goes by
  * s_e, or by s_e + bias_e with a bias: the k largest in descending order, ties
- * to the lowest index, NaN before all.  A score of -inf (logit or bias) is
- * never chosen: a token with fewer than k others has slots of no expert.
+ * to the lowest index, NaN before all.  A logit of -inf is never chosen, nor a
+ * bias of -inf unless its s_e is NaN (one NaN or +inf makes all of a token's
+ * softmax NaN): a token with fewer than k others has slots of no expert.
  *   weight = weight_scale * s_e, or weight_scale * s_e / (sum of the token's
  *            chosen s) with normalize != 0 (0 where that sum is 0); the softmax runs
  *            over all E, also with a bias; 0 for slots of no expert.  Computed in 64

@@ -8,8 +8,6 @@
 namespace ar {
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 __device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
 // ------------------------------------------------------------- choice ------
@@ -428,7 +426,12 @@ __global__ void __launch_bounds__(kOrderThreads) moe_rank_kernel(MoeRouteArgs a,
 }
 
 // A few tokens in one launch: a workgroup's 16 wavefronts choose for a token
-// each in turn, then order the slots: 1 token of 64 experts 4.5 + 3.2 -> 5 us.
+// each in turn, then order the slots.  Captured, one launch and two (us): 1 token
+// of 64 experts 5.2 and 5.9, of 256 6.0 and 6.9, of 1024 10.8 and 12.2; 4 of 256
+// 6.2 and 7.1; 16 of 64 6.3 and 6.3, of 256 7.9 and 7.3, of 1024 24 and 14; 32 of
+// 64 8.8 and 6.4, of 256 11.4 and 7.3, of 1024 34 and 14 (a workgroup of 1024
+// threads leaves 128 registers: 18 are spilled for up to 512 experts, 52 above).
+// So from about 8 tokens on two launches are the faster form of a captured call.
 constexpr int kFewTokens = 32, kFewSlots = kFewTokens * kMoeMaxChoices;
 
 template <int V>
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(kOrderThreads) moe_few_kernel(MoeRouteArgs a) 
 // fp32 with one rounding at the end.  A thread has C neighbouring columns: four,
 // 8 bytes of bf16, where all operands are aligned for it, else one.  Every row of
 // z is read once and y written once, which bounds it: 4096 tokens of 8 experts,
-// 4100 wide, bf16 to fp32, 67 us (4.6 TB/s).  A thread that goes on to further
+// 4100 wide, bf16 to fp32, 67 us (4.6 TB/s), 4101 wide, by single columns, 179.  A thread that goes on to further
 // columns or tokens in a loop is slower (101 us), so a workgroup has one piece.
 template <int C, bool BF16>
 __device__ __forceinline__ void load_cols(float (&v)[C], const void* p, int64_t at) {

@@ -23,6 +23,10 @@ namespace ar {
 //   32768 x 128 x 4096 x 2048 (256): 256x256 584, 64x256 652, 128x128 686
 //   4096 x 8 x 11008 x 4096 (512): 256x256 367, 128x128 358; gathered from 2048 tokens, with bias and SiLU 382 and 402
 //   32768 x 32 x 4096 x 4096 (1024): 256x256 926, 128x256 1040, 128x128 1081
+// 256x256 and 128x128 by the 256x256 tiles to expect, of which more than 768 are several rounds:
+//   320 (4096 x 8 x 4096 x 4096) 175 and 147; 516 (2048 x 8 x 11008 x 4096) 257 and 197; 640 (4096 x 8 x 8192 x 4096)
+//   257 and 262, (8192 x 16 x 4096 x 4096) 269 and 262; 768 (8192 x 32 x 4096 x 4096) 353 and 297; 860 (4096 x 8 x 11008
+//   x 4096) 369 and 373; 1280 (16384 x 32 x 4096 x 2048) 251 and 268
 hipError_t launch_mx_grouped_a16(const MxGroupArgs& a, hipStream_t stream) {
     const int64_t mean = a.M / a.E;
     if (likely_tiles(a, 32, 128) <= 256) launch_groups<false, 32, 64, 1, 2, 2, 8, 3>(a, stream);

@@ -14,6 +14,9 @@ namespace ar {
 //   8192 x 64 x 4096 x 2048 (128): 128x128 112, 256x256 113, 64x128 134
 //   32768 x 128 x 4096 x 2048 (256): 256x256 303, 128x128 361, 64x128 490
 //   32768 x 32 x 4096 x 4096 (1024): 256x256 372, 128x128 447
+//   few experts: the rule does not count whether 256x256 tiles fill the CUs.  256x256 (taken) and 128x128: 512 x 2 x 4096
+//   x 4096 (256) 28 and 14; 1024 x 4 x 4096 x 4096 (256) 29 and 22; 1600 x 8 x 4096 x 2048 (200) 21 and 16; 2048 x 8 x
+//   4096 x 4096 (256) 33 and 38; 4096 x 8 x 4096 x 4096 (512) 63 and 58; 4096 x 8 x 11008 x 4096 (512) 134 and 138
 //   K 2080: 3000 x 16 x 4096 (188): 128x128 67, 64x64 77, 32x64 96; 700 x 5 x 1000 (140): 32x64 10, 64x64 11
 hipError_t launch_mx_grouped_a4(const MxGroupArgs& a, hipStream_t stream) {
     const bool aligned = a.K % 128 == 0 && a.K >= 256 &&

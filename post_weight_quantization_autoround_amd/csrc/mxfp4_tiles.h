@@ -74,9 +74,9 @@ template <class Args> inline constexpr bool kMxGrouped = std::is_same_v<Args, Mx
 //              subnormal number here for v < -13, would lose those results' bits)
 // For bf16 results the exponential is the hardware's 2^x of x log2(e) and the
 // quotient a product with its reciprocal: together at most 2^-16 relative
-// (x log2(e) rounds by 2^-24 |x|, |x| <= 52 where h is not 0, and counts
-// twice), far below bf16's half step of 2^-8; fp32 results take expf and a
-// division.
+// (x log2(e) is off by at most 2^-23 |x|, its own rounding and its constant's,
+// and counts twice; the result v h^2 is 0 for |x| = |u| / 2 > 55), far below
+// bf16's half step of 2^-8; fp32 results take expf and a division.
 // v sigmoid(u):
 template <bool BF16>
 __device__ __forceinline__ float mx_gate(float v, float u) {
@@ -155,8 +155,10 @@ struct MxFour {
     }
 };
 
-// STREAM: past the L2, whose lines the large tiles' operands need (32768 x 4096
-// x 2048 over 128 experts 4 to 8% shorter).
+// STREAM: past the L2, whose lines the tiles' operands need (packed X, us, past
+// it and into it: 4096 x 32768 x 8192 511 and 549, 512 x 11008 x 4096 20.2 and
+// 21.1; grouped 32768 x 4096 x 2048 over 128 experts 288 and 293, 512 x 2048 x
+// 4096 over 128 101.1 and 101.8, with the gate that reads it 112.7 and 112.6).
 template <bool BF16, bool STREAM>
 __device__ __forceinline__ void mx_store_four(void* y, f32x4 v, bool wide, int64_t left) {
     if (wide) {
@@ -1270,8 +1272,14 @@ hipError_t launch_a16(const Args& a, hipStream_t stream) {
     else if (tiles(a, 128, 256) <= 256) launch_ring<false, 128, 256, 2, 4, 1, 4, 3>(a, stream);
     else {
         // Several rounds: 256x256 is 6% faster a flop, 128x256 (two workgroups a
-        // CU, so at most 128 registers, two of them spilled outside the K loop)
-        // fills its last round better.
+        // CU, so at most 128 registers) fills its last round better.  The plain
+        // form spills two registers, outside the K loop, the one with an epilogue
+        // 136 (fp32 Y: 143), one of which it loads in the loop.  128x256 against
+        // 256x256 there, without an epilogue, with bias and SiLU, with a residual:
+        // 2048 x 11008 x 4096 159, 169, 171 against 175, 184, 195; 4096 x 6144 x
+        // 4096 171, 181, 183 against 181, 188, 199; 4096 x 14336 x 4096 384, 402,
+        // 408 against 381, 401, 425; 2048 x 28672 x 8192 749, 765, 782 against
+        // 721, 736, 784 (the rule takes 128x256 in all of them).
         const int64_t big = tiles(a, 256, 256), small = tiles(a, 128, 256);
         const double full_big = (double)big / (double)((big + 255) / 256), full_small = (double)small / (double)((small + 255) / 256);
         if (1.06 * full_big >= full_small) launch_ring<false, 256, 256, 2, 4, 1, 2, 3>(a, stream);
